@@ -325,6 +325,155 @@ MOE_API moe_status moe_combine(const uint16_t* y_perm, const int32_t* slot_pos,
                        const float* topk_w, moe_shape shape, uint16_t* out,
                        moe_stream stream);
 
+/* mxfp4_transposed_width -- positions of a transposed MXFP4 matrix along its
+ * contraction axis (the axis that was `rows`): rows rounded up to 32 for E = 0
+ * (mxfp4_quantize_transposed), and for E >= 1 groups of rows
+ * (mxfp4_quantize_transposed_grouped) the smallest multiple of 128 that holds
+ * every split of `rows` into E groups, each rounded up to a multiple of 128:
+ * floor((rows + 127 E) / 128) * 128.
+ * Returns 0 for rows outside [0, 2^31] or E outside [0, 256].  Host only.  */
+MOE_API int64_t mxfp4_transposed_width(int64_t rows, int32_t E);
+
+/* mxfp4_quantize_transposed -- bf16 -> MXFP4 of the transpose.
+ * Passage: "MXFP4-based MoE technical review", section 2 (training in MXFP4):
+ * a block-scaled product takes its blocks along the axis it sums over, so the
+ * two backward products of a linear map need their operands quantised along
+ * the other axis.  Format and rounding are mxfp4_quantize's: for every matrix
+ * b the bytes are those of mxfp4_quantize applied to w[b] transposed, with the
+ * positions from `rows` to P zero.
+ *   w_bf16   in   [batch][rows][cols] bf16
+ *   batch    in   >= 0;  rows in >= 0 (either 0: a no-op), rows <= 2^31
+ *   cols     in   multiple of 8, >= 8;  batch*rows*cols <= 2^40
+ *   q_packed out  [batch][cols][P/2], P = mxfp4_transposed_width(rows, 0)
+ *   scales   out  [batch][cols][P/32]
+ *   d_status out  nullable; MOE_ERR_NONFINITE if a block holds NaN or Inf
+ *                 (its bytes unspecified); never written otherwise.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED,
+ * MOE_ERR_CUDA.                                                          */
+MOE_API moe_status mxfp4_quantize_transposed(const uint16_t* w_bf16, int64_t batch, int64_t rows,
+                                             int64_t cols, uint8_t* q_packed, uint8_t* scales,
+                                             int32_t* d_status, moe_stream stream);
+
+/* mxfp4_quantize_transposed_grouped -- the same for rows sorted by expert.
+ * Group e (rows [offsets[e], offsets[e+1]) of w) takes the positions that
+ * start at 128 * sum over i < e of ceil(count_i / 128); no block and no group
+ * of 128 positions meets two groups.  A group's positions from its last row to
+ * the next multiple of 128 are zero; positions behind the last group are left
+ * as they were (mxfp4_matmul_grouped_wgrad reads none of them).
+ *   w_bf16   in   [rows][cols] bf16, cols a multiple of 8
+ *   offsets  in   [E+1] device, ascending, in [0, rows], 1 <= E <= 256; rows in
+ *                 no group are not read
+ *   q_packed out  [cols][P/2], P = mxfp4_transposed_width(rows, E)
+ *   scales   out  [cols][P/32];  d_status as above
+ * Errors: as mxfp4_quantize_transposed.                                  */
+MOE_API moe_status mxfp4_quantize_transposed_grouped(const uint16_t* w_bf16, int64_t rows,
+                                                     int64_t cols, const int32_t* offsets,
+                                                     int32_t E, uint8_t* q_packed, uint8_t* scales,
+                                                     int32_t* d_status, moe_stream stream);
+
+/* Type of a product's output. */
+#define MOE_OUT_BF16 0
+#define MOE_OUT_FP32 1
+
+/* mxfp4_matmul -- product of two MXFP4 matrices.
+ * Passage: "MXFP4-based MoE technical review", section 2 (training in MXFP4);
+ * "Tricks from OpenAI gpt-oss ..." (summary), section 8 (GEMMs that read the
+ * blocks and their scales directly).
+ * out[m][n] = alpha * sum_k A[m][k] * B[n][k]: exact products of the scaled
+ * elements, fp32 accumulation in a fixed but unspecified order, one rounding
+ * to the output type.  Operands of mxfp4_quantize_sr_rht with the same
+ * transform along K are multiplied with alpha = 1/32.  A scale byte 255 is
+ * NaN.
+ *   a_q, a_s in   MXFP4 [M][K];  b_q, b_s in MXFP4 [N][K]
+ *   M, N     in   [0, 2^27] (0: a no-op);  K a multiple of 32 in [32, 2^24]
+ *   out      out  [M][N], out_type MOE_OUT_BF16 or MOE_OUT_FP32
+ *   d_status out  nullable; MOE_ERR_TIMEOUT if a bounded wait gave up (never
+ *                 written otherwise)
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED,
+ * MOE_ERR_CUDA.                                                          */
+MOE_API moe_status mxfp4_matmul(const uint8_t* a_q, const uint8_t* a_s, const uint8_t* b_q,
+                                const uint8_t* b_s, int64_t M, int64_t N, int64_t K, float alpha,
+                                void* out, int32_t out_type, int32_t* d_status, moe_stream stream);
+
+/* mxfp4_matmul_grouped -- the product of every expert's rows with its matrix.
+ * For every row r in [offsets[e], offsets[e+1]):
+ *   out[r][n] = alpha * sum_k A[r][k] * B[e][n][k]
+ * with A's rows in moe_permute's order, quantised by mxfp4_quantize.  Rows of
+ * `out` in no group are left as they were.  The backward product with respect
+ * to A is this call on the gradient's rows and the matrices of
+ * mxfp4_quantize_transposed.
+ *   a_q, a_s in   MXFP4 [S][K];  offsets in [E+1] device, ascending, in [0, S]
+ *   b_q, b_s in   MXFP4 [E][N][K], 1 <= E <= 256, E*N <= 2^27
+ *   S        in   [0, 2^27];  K a multiple of 32 in [32, 2^24]
+ *   out      out  [S][N];  out_type, d_status as mxfp4_matmul
+ * Errors: as mxfp4_matmul.                                               */
+MOE_API moe_status mxfp4_matmul_grouped(const uint8_t* a_q, const uint8_t* a_s,
+                                        const int32_t* offsets, int32_t E, const uint8_t* b_q,
+                                        const uint8_t* b_s, int64_t S, int64_t N, int64_t K,
+                                        float alpha, void* out, int32_t out_type,
+                                        int32_t* d_status, moe_stream stream);
+
+/* mxfp4_matmul_grouped_wgrad -- every expert's weight gradient.
+ *   out[e][m][n] = alpha * sum over the positions p of group e of
+ *                  A[m][p] * B[n][p]
+ * A and B as mxfp4_quantize_transposed_grouped leaves the gradient's rows and
+ * the input's rows for the same offsets.  An expert without rows gets zeros.
+ *   a_q, a_s in   MXFP4 [M][P];  b_q, b_s in MXFP4 [N][P]
+ *   offsets  in   [E+1] device, the row offsets given to the quantiser
+ *   P        in   multiple of 128 in [0, 2^24] (mxfp4_transposed_width(rows,
+ *                 E)); nothing at or behind P is read, whatever the offsets hold
+ *   M, N     in   E*M <= 2^27, N <= 2^27, 1 <= E <= 256
+ *   out      out  [E][M][N];  out_type, d_status as mxfp4_matmul
+ * Errors: as mxfp4_matmul.                                               */
+MOE_API moe_status mxfp4_matmul_grouped_wgrad(const uint8_t* a_q, const uint8_t* a_s,
+                                              const uint8_t* b_q, const uint8_t* b_s,
+                                              const int32_t* offsets, int32_t E, int64_t M,
+                                              int64_t N, int64_t P, float alpha, void* out,
+                                              int32_t out_type, int32_t* d_status,
+                                              moe_stream stream);
+
+/* moe_combine_backward -- gradient of moe_combine and of moe_route's softmax.
+ * Passage: "Welcome GPT OSS ..." (summary), section 4 (the softmax over the
+ * chosen experts mixes their outputs).  With p = slot_pos[t*k+j]:
+ *   dy_perm[p][d]  = bf16_rne( topk_w[t][j] * dout[t][d] )
+ *   dtopk_w[t][j]  = sum_d dout[t][d] * y_perm[p][d]            (fp32)
+ *   dscore[t][j]   = topk_w[t][j] * ( dtopk_w[t][j]
+ *                                     - sum_i topk_w[t][i] * dtopk_w[t][i] )
+ * dscore is the gradient of the k chosen logits when topk_w is their softmax
+ * (the other logits have none).  A slot whose slot_pos is outside [0, S) was
+ * dropped: it writes no row and its dtopk_w is 0.  Rows of dy_perm that no
+ * slot maps to are left as they were.  Two slots must not share a position.
+ *   dout     in   [T][D] bf16;  y_perm in [S][D] bf16, may be NULL when neither
+ *                 dtopk_w nor dscore is asked for
+ *   slot_pos in   [S];  topk_w in [T][k] fp32
+ *   dy_perm  out  [S][D] bf16
+ *   dtopk_w, dscore out  nullable; [T][k] fp32
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED,
+ * MOE_ERR_CUDA.                                                          */
+MOE_API moe_status moe_combine_backward(const uint16_t* dout, const uint16_t* y_perm,
+                                        const int32_t* slot_pos, const float* topk_w,
+                                        moe_shape shape, uint16_t* dy_perm, float* dtopk_w,
+                                        float* dscore, moe_stream stream);
+
+/* moe_permute_backward -- gradient of moe_permute's row gather, with the
+ * router's share.
+ * Passage: "MXFP4-based MoE technical review", section 4 (routing over sparse
+ * experts); "Welcome GPT OSS ..." (summary), section 4.
+ * dx[t][d] = bf16_rne( sum_j dx_perm[slot_pos[t*k+j]][d]
+ *                      + sum_j dscore[t][j] * w_router[topk_idx[t][j]][d] )
+ * summed in fp32 in a fixed order (the rows first, j ascending); the second sum
+ * only when the three router arguments are given (all or none).  A slot_pos
+ * outside [0, S) or a topk_idx outside [0, E) contributes nothing.
+ *   dx_perm  in   [S][D] bf16;  slot_pos in [S];  dx out [T][D] bf16
+ *   topk_idx in   nullable; [T][k] int32;  dscore in nullable; [T][k] fp32
+ *   w_router in   nullable; [E][D] bf16 (moe_router_topk's)
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED,
+ * MOE_ERR_CUDA.                                                          */
+MOE_API moe_status moe_permute_backward(const uint16_t* dx_perm, const int32_t* slot_pos,
+                                        moe_shape shape, uint16_t* dx, const int32_t* topk_idx,
+                                        const float* dscore, const uint16_t* w_router,
+                                        moe_stream stream);
+
 /* moe_layer_forward -- the whole layer: moe_route -> moe_permute ->
  * moe_expert_mlp -> moe_combine, enqueued on one stream, all intermediates
  * in the caller's workspace (moe_workspace_size(shape, 2) bytes).

@@ -37,6 +37,10 @@ MOE_QUANT_RHT = 1  # random-sign Hadamard transform of each 32-block along K
 MOE_QUANT_SR = 2   # stochastic rounding
 
 
+MOE_OUT_BF16 = 0  # output type of a product
+MOE_OUT_FP32 = 1
+
+
 class MoeError(RuntimeError):
     def __init__(self, fn: str, status: int):
         super().__init__(f"{fn}: {moe_status_string(status)} ({status})")
@@ -79,6 +83,25 @@ def _load() -> ctypes.CDLL:
     lib.moe_expert_mlp_unquantised.restype = st
     lib.moe_combine.argtypes = [vp, vp, vp, moe_shape, vp, vp]
     lib.moe_combine.restype = st
+    f32 = ctypes.c_float
+    lib.mxfp4_transposed_width.argtypes = [i64, i32]
+    lib.mxfp4_transposed_width.restype = i64
+    lib.mxfp4_quantize_transposed.argtypes = [vp, i64, i64, i64, vp, vp, vp, vp]
+    lib.mxfp4_quantize_transposed.restype = st
+    lib.mxfp4_quantize_transposed_grouped.argtypes = [vp, i64, i64, vp, i32, vp, vp, vp, vp]
+    lib.mxfp4_quantize_transposed_grouped.restype = st
+    lib.mxfp4_matmul.argtypes = [vp, vp, vp, vp, i64, i64, i64, f32, vp, i32, vp, vp]
+    lib.mxfp4_matmul.restype = st
+    lib.mxfp4_matmul_grouped.argtypes = [vp, vp, vp, i32, vp, vp, i64, i64, i64, f32, vp, i32, vp,
+                                         vp]
+    lib.mxfp4_matmul_grouped.restype = st
+    lib.mxfp4_matmul_grouped_wgrad.argtypes = [vp, vp, vp, vp, vp, i32, i64, i64, i64, f32, vp, i32,
+                                               vp, vp]
+    lib.mxfp4_matmul_grouped_wgrad.restype = st
+    lib.moe_combine_backward.argtypes = [vp, vp, vp, vp, moe_shape, vp, vp, vp, vp]
+    lib.moe_combine_backward.restype = st
+    lib.moe_permute_backward.argtypes = [vp, vp, moe_shape, vp, vp, vp, vp, vp]
+    lib.moe_permute_backward.restype = st
     lib.moe_layer_forward.argtypes = [vp, vp, moe_shape, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.moe_layer_forward.restype = st
     lib.moe_layer_forward_static.argtypes = [vp, vp, moe_shape, vp, vp, vp, vp, vp, vp]
@@ -162,6 +185,102 @@ def mxfp4_quantize_sr_rht(w_bf16, flags: int, rht_signs, seed: int, q_packed, sc
                                      _p(d_status), _s(stream)))
 
 
+def _sizes(fn: str, ok: bool) -> None:
+    """Shapes that contradict one another are refused before the C call, which
+    would otherwise read or write past the smaller one."""
+    if not ok:
+        raise ValueError(f"{fn}: the tensors' shapes or types do not belong together")
+
+
+def _out_type(fn: str, out) -> int:
+    import torch
+
+    if out.dtype == torch.bfloat16:
+        return MOE_OUT_BF16
+    if out.dtype == torch.float32:
+        return MOE_OUT_FP32
+    raise ValueError(f"{fn}: the output is bfloat16 or float32, not {out.dtype}")
+
+
+def _mx_ok(q, s, K: int) -> bool:
+    import torch
+
+    return (q.dtype == torch.uint8 and s.dtype == torch.uint8 and q.shape[:-1] == s.shape[:-1]
+            and 2 * q.shape[-1] == K and 32 * s.shape[-1] == K)
+
+
+def mxfp4_transposed_width(rows: int, E: int = 0) -> int:
+    """Positions along the contraction axis of a transposed MXFP4 matrix: rows
+    rounded up to 32, or, with E groups of rows, room for each of them to start
+    at a multiple of 128."""
+    return int(lib.mxfp4_transposed_width(int(rows), int(E)))
+
+
+def mxfp4_quantize_transposed(w_bf16, q_packed, scales, d_status=None, stream=None) -> None:
+    """w_bf16 [..., R, C] bf16 -> q_packed [..., C, P/2] u8, scales [..., C, P/32] u8,
+    P = mxfp4_transposed_width(R): mxfp4_quantize of the transpose."""
+    fn = "mxfp4_quantize_transposed"
+    R, C = w_bf16.shape[-2:]
+    P = mxfp4_transposed_width(R)
+    _sizes(fn, w_bf16.element_size() == 2 and _mx_ok(q_packed, scales, P)
+           and q_packed.shape[:-1] == w_bf16.shape[:-2] + (C,))
+    batch = w_bf16.numel() // (R * C) if R * C else 0
+    _check(fn, lib.mxfp4_quantize_transposed(_p(w_bf16), batch, R, C, _p(q_packed), _p(scales),
+                                             _p(d_status), _s(stream)))
+
+
+def mxfp4_quantize_transposed_grouped(w_bf16, offsets, q_packed, scales, d_status=None,
+                                      stream=None) -> None:
+    """w_bf16 [S, C] bf16, offsets [E+1] i32 -> q_packed [C, P/2], scales [C, P/32],
+    P = mxfp4_transposed_width(S, E), every group at a multiple of 128 positions."""
+    fn = "mxfp4_quantize_transposed_grouped"
+    S, C = w_bf16.shape
+    E = offsets.numel() - 1
+    P = mxfp4_transposed_width(S, E)
+    _sizes(fn, w_bf16.element_size() == 2 and offsets.element_size() == 4
+           and _mx_ok(q_packed, scales, P) and tuple(q_packed.shape[:-1]) == (C,))
+    _check(fn, lib.mxfp4_quantize_transposed_grouped(_p(w_bf16), S, C, _p(offsets), E,
+                                                     _p(q_packed), _p(scales), _p(d_status),
+                                                     _s(stream)))
+
+
+def mxfp4_matmul(a_q, a_s, b_q, b_s, out, alpha: float = 1.0, d_status=None, stream=None) -> None:
+    """out [M, N] (bf16 or fp32) = alpha * A B^T of MXFP4 A [M, K] and B [N, K]."""
+    fn = "mxfp4_matmul"
+    (M, N), K = out.shape, 2 * a_q.shape[-1]
+    _sizes(fn, _mx_ok(a_q, a_s, K) and _mx_ok(b_q, b_s, K) and tuple(a_q.shape[:-1]) == (M,)
+           and tuple(b_q.shape[:-1]) == (N,))
+    _check(fn, lib.mxfp4_matmul(_p(a_q), _p(a_s), _p(b_q), _p(b_s), M, N, K, float(alpha), _p(out),
+                                _out_type(fn, out), _p(d_status), _s(stream)))
+
+
+def mxfp4_matmul_grouped(a_q, a_s, offsets, b_q, b_s, out, alpha: float = 1.0, d_status=None,
+                         stream=None) -> None:
+    """out [S, N] = alpha * (rows of group e of A [S, K]) B_e^T, B [E, N, K], groups by
+    offsets [E+1]; rows in no group are left as they were."""
+    fn = "mxfp4_matmul_grouped"
+    (S, N), K, E = out.shape, 2 * a_q.shape[-1], offsets.numel() - 1
+    _sizes(fn, _mx_ok(a_q, a_s, K) and _mx_ok(b_q, b_s, K) and tuple(a_q.shape[:-1]) == (S,)
+           and tuple(b_q.shape[:-1]) == (E, N) and offsets.element_size() == 4)
+    _check(fn, lib.mxfp4_matmul_grouped(_p(a_q), _p(a_s), _p(offsets), E, _p(b_q), _p(b_s), S, N, K,
+                                        float(alpha), _p(out), _out_type(fn, out), _p(d_status),
+                                        _s(stream)))
+
+
+def mxfp4_matmul_grouped_wgrad(a_q, a_s, b_q, b_s, offsets, out, alpha: float = 1.0, d_status=None,
+                               stream=None) -> None:
+    """out [E, M, N] = alpha * A_e B_e^T over the positions of group e of A [M, P] and
+    B [N, P] (mxfp4_quantize_transposed_grouped's outputs for the same offsets)."""
+    fn = "mxfp4_matmul_grouped_wgrad"
+    (E, M, N), P = out.shape, 2 * a_q.shape[-1]
+    _sizes(fn, _mx_ok(a_q, a_s, P) and _mx_ok(b_q, b_s, P) and tuple(a_q.shape[:-1]) == (M,)
+           and tuple(b_q.shape[:-1]) == (N,) and offsets.numel() == E + 1
+           and offsets.element_size() == 4)
+    _check(fn, lib.mxfp4_matmul_grouped_wgrad(_p(a_q), _p(a_s), _p(b_q), _p(b_s), _p(offsets), E, M,
+                                              N, P, float(alpha), _p(out), _out_type(fn, out),
+                                              _p(d_status), _s(stream)))
+
+
 def moe_route(logits, k: int, topk_idx, topk_w, stream=None) -> None:
     T, E = logits.shape
     _check("moe_route", lib.moe_route(_p(logits), T, E, k, _p(topk_idx), _p(topk_w), _s(stream)))
@@ -218,6 +337,24 @@ def moe_combine(y_perm, slot_pos, topk_w, shape: moe_shape, out, stream=None) ->
                                           _s(stream)))
 
 
+def moe_combine_backward(dout, y_perm, slot_pos, topk_w, shape: moe_shape, dy_perm, dtopk_w=None,
+                         dscore=None, stream=None) -> None:
+    """Gradients of moe_combine: dy_perm [S][D], dtopk_w [T][k], and dscore [T][k] of the
+    k chosen logits through the softmax (the last two when given)."""
+    _check("moe_combine_backward",
+           lib.moe_combine_backward(_p(dout), _p(y_perm), _p(slot_pos), _p(topk_w), shape,
+                                    _p(dy_perm), _p(dtopk_w), _p(dscore), _s(stream)))
+
+
+def moe_permute_backward(dx_perm, slot_pos, shape: moe_shape, dx, topk_idx=None, dscore=None,
+                         w_router=None, stream=None) -> None:
+    """Gradient of moe_permute's gather: dx [T][D], plus the router's share when
+    topk_idx [T][k], dscore [T][k] and w_router [E][D] are given."""
+    _check("moe_permute_backward",
+           lib.moe_permute_backward(_p(dx_perm), _p(slot_pos), shape, _p(dx), _p(topk_idx),
+                                    _p(dscore), _p(w_router), _s(stream)))
+
+
 def moe_layer_forward(x, logits, shape: moe_shape, wgu_q, wgu_s, wdn_q, wdn_s, out, ws,
                       stream=None) -> None:
     _check("moe_layer_forward", lib.moe_layer_forward(_p(x), _p(logits), shape, _p(wgu_q),
@@ -252,7 +389,11 @@ def alloc_workspace(shape: moe_shape, which: int, device="cuda"):
 
 
 __all__ = ["moe_shape", "make_shape", "MoeError", "mxfp4_quantize", "mxfp4_quantize_sr_rht",
-           "MOE_QUANT_RHT", "MOE_QUANT_SR", "moe_route",
+           "MOE_QUANT_RHT", "MOE_QUANT_SR",
+           "mxfp4_transposed_width", "mxfp4_quantize_transposed",
+           "mxfp4_quantize_transposed_grouped", "mxfp4_matmul", "mxfp4_matmul_grouped",
+           "mxfp4_matmul_grouped_wgrad", "MOE_OUT_BF16", "MOE_OUT_FP32",
+           "moe_combine_backward", "moe_permute_backward", "moe_route",
            "moe_router_topk", "moe_permute",
            "moe_expert_mlp", "moe_expert_mlp_ex", "moe_expert_mlp_unquantised", "moe_combine", "moe_layer_forward",
            "moe_layer_forward_static", "moe_layer_static_status",

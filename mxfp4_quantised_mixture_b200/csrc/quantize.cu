@@ -21,28 +21,13 @@
 // element the kernel is a stream bound by HBM (2 bytes read, 17/32 byte
 // written per element).
 #include "common.cuh"
+#include "e2m1.cuh"
 
 namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kUnroll = 4;
-
-// E2M1 codes of 8 fp32 values (element 0 in the low nibble of the result)
-__device__ __forceinline__ uint32_t cvt_e2m1x8(const float (&f)[8]) {
-  uint32_t out;
-  asm("{\n"
-      ".reg .b8 c0, c1, c2, c3;\n"
-      "cvt.rn.satfinite.e2m1x2.f32 c0, %2, %1;\n"
-      "cvt.rn.satfinite.e2m1x2.f32 c1, %4, %3;\n"
-      "cvt.rn.satfinite.e2m1x2.f32 c2, %6, %5;\n"
-      "cvt.rn.satfinite.e2m1x2.f32 c3, %8, %7;\n"
-      "mov.b32 %0, {c0, c1, c2, c3};\n"
-      "}"
-      : "=r"(out)
-      : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
-  return out;
-}
 
 __device__ __forceinline__ uint32_t encode8(uint4 v, float inv_scale) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -87,11 +72,8 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const uint4* __restr
       uint32_t m = max_magnitude8(v[u]);
       m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
       m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-      const int bexp = static_cast<int>(m >> 7);
-      const int sb = max(bexp - 2, 0);  // <= 252 for finite input
-      // 2^(127 - sb) as an fp32 bit pattern (sb <= 253 keeps it finite)
-      const float inv_scale = __uint_as_float(static_cast<uint32_t>(254 - min(sb, 253)) << 23);
-      const uint32_t packed = encode8(v[u], inv_scale);
+      const int sb = scale_byte(m);
+      const uint32_t packed = encode8(v[u], inverse_scale(sb));
       if (valid) q[i] = packed;
       if (m >= 0x7F80u && valid) record_status(status, MOE_ERR_NONFINITE);
       // scale bytes: lanes 0,4,..,28 hold the scales of 8 consecutive blocks

@@ -1,0 +1,192 @@
+// bf16 -> MXFP4 along the other axis: the transpose of the input, quantised in
+// blocks of 32 along what were its rows.
+//
+// "MXFP4-based MoE technical review", section 2 (MXFP4 training): a block-scaled
+// product needs its blocks along the axis it sums over, and a linear map's two
+// backward products sum over the other axes than its forward product, so their
+// operands are quantised again, transposed.  Format and rounding are those of
+// mxfp4_quantize (csrc/quantize.cu).
+//
+// One CTA takes 128 rows x 128 columns.  A lane owns two neighbouring columns
+// (one 32-bit word) of one 32-row block: 32 loads, each of them 128 contiguous
+// bytes per warp, all in flight at once; the block maximum is then a maximum
+// over the lane's own registers, with no shuffle.  The codes (16 bytes per
+// column and block) go through shared memory so that the four blocks of a
+// column leave as one 64-byte run.  HBM-bound: 2 bytes read and 17/32 byte
+// written per element.
+//
+// Grouped rows (a ragged batch sorted by expert): the output positions of a
+// group start at a multiple of 128 and are zero behind its last row, so a
+// product over one group's positions never meets another's, and a 128-row tile
+// belongs to one group.
+#include "common.cuh"
+#include "e2m1.cuh"
+#include "groups.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRows = 128, kCols = 128;
+
+template <bool GROUPED>
+__global__ void __launch_bounds__(kThreads)
+    quantize_transposed_kernel(const uint32_t* __restrict__ w, int64_t rows, int64_t cols,
+                               int64_t batch, const int32_t* __restrict__ offsets, int E, int64_t P,
+                               uint8_t* __restrict__ q, uint8_t* __restrict__ s,
+                               int32_t* __restrict__ status) {
+  __shared__ uint4 codes[kCols * 4];
+  __shared__ uint32_t scales[kCols];
+  __shared__ int64_t pfx[kMaxGroups + 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rb = warp & 3;                       // 32-row block of the tile
+  const int lc = (warp >> 2) * 64 + lane * 2;    // first of this lane's two columns
+  const int64_t col_tiles = (cols + kCols - 1) / kCols;
+  int64_t row_tiles = (P + kRows - 1) / kRows;
+  if (GROUPED) {
+    if (warp == 0)
+      group_prefix(E, pfx, [&](int e) {
+        int64_t lo, hi;
+        group_rows(offsets, e, rows, lo, hi);
+        return (hi - lo + kGroupAlign - 1) / kGroupAlign;
+      });
+    __syncthreads();
+    row_tiles = min(row_tiles, pfx[E]);
+  }
+  const int64_t n_tiles = batch * row_tiles * col_tiles;
+  for (int64_t i = blockIdx.x; i < n_tiles; i += gridDim.x) {
+    const int64_t ct = i % col_tiles;
+    const int64_t rt = i / col_tiles % row_tiles;
+    const int64_t b = i / col_tiles / row_tiles;
+    int64_t r0 = rt * kRows, r_end = rows;  // source rows of the tile: [r0, r_end)
+    if (GROUPED) {
+      const int e = group_of(pfx, E, rt);
+      int64_t lo;
+      group_rows(offsets, e, rows, lo, r_end);
+      r0 = lo + (rt - pfx[e]) * kRows;
+    }
+    const int64_t c0 = ct * kCols;
+    const bool col_ok = c0 + lc < cols;  // cols is even
+    const int64_t rs = r0 + rb * 32;
+    const uint32_t* src = w + (b * rows + rs) * (cols / 2) + (c0 + lc) / 2;
+    uint32_t v[32];
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+      v[k] = col_ok && rs + k < r_end ? __ldg(src + k * (cols / 2)) : 0u;
+    uint32_t m2 = 0;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) m2 = __vmaxu2(m2, v[k] & 0x7FFF7FFFu);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t m = h ? m2 >> 16 : m2 & 0xFFFFu;
+      const int sb = scale_byte(m);
+      const float inv = inverse_scale(sb);
+      uint32_t c[4];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        float f[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t x = v[8 * g + k];
+          f[k] = __uint_as_float(h ? x & 0xFFFF0000u : x << 16) * inv;
+        }
+        c[g] = cvt_e2m1x8(f);
+      }
+      // 128-byte lines of two columns, their 16-byte slots permuted by the
+      // line so that neither side meets a bank conflict
+      const int line = (lc + h) >> 1;
+      codes[line * 8 + ((h * 4 + rb) ^ (line & 7))] = make_uint4(c[0], c[1], c[2], c[3]);
+      reinterpret_cast<uint8_t*>(scales)[(lc + h) * 4 + rb] = static_cast<uint8_t>(sb);
+      if (m >= 0x7F80u) record_status(status, MOE_ERR_NONFINITE);
+    }
+    __syncthreads();
+    const int64_t p0 = rt * kRows;  // first output position
+    for (int j = threadIdx.x; j < kCols * 4; j += kThreads) {
+      const int col = j >> 2, blk = j & 3, line = col >> 1;
+      if (c0 + col < cols && p0 + blk * 32 < P)
+        *reinterpret_cast<uint4*>(q + (b * cols + c0 + col) * (P / 2) + p0 / 2 + blk * 16) =
+            codes[line * 8 + (((col & 1) * 4 + blk) ^ (line & 7))];
+    }
+    for (int j = threadIdx.x; j < kCols; j += kThreads) {
+      if (c0 + j >= cols) continue;
+      uint8_t* dst = s + (b * cols + c0 + j) * (P / 32) + p0 / 32;
+      if (P % 128 == 0) {
+        *reinterpret_cast<uint32_t*>(dst) = scales[j];
+      } else {
+        for (int blk = 0; blk < 4; ++blk)
+          if (p0 + blk * 32 < P) dst[blk] = static_cast<uint8_t>(scales[j] >> (8 * blk));
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// Checks shared by both entries; `need_offsets` for the grouped one.
+moe_status check(const uint16_t* w, int64_t n, const uint8_t* q, const uint8_t* s,
+                 const int32_t* d_status) {
+  if (n > 0 && (!w || !q || !s)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(w) || !aligned16(q) || !aligned16(s)) return MOE_ERR_INVALID_ARG;
+  if (d_status && (reinterpret_cast<uintptr_t>(d_status) & 3u)) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+int grid_for(int64_t tiles) {
+  const int64_t cap = static_cast<int64_t>(sm_count()) * 8;
+  return static_cast<int>(tiles < cap ? tiles : cap);
+}
+
+bool sizes_ok(int64_t batch, int64_t rows, int64_t cols) {
+  if (batch < 0 || rows < 0 || cols < 8 || cols % 8) return false;
+  const int64_t lim = int64_t(1) << 40;
+  if (rows > (int64_t(1) << 31) || cols > lim || batch > lim) return false;
+  if (rows > 0 && (cols > lim / rows || (batch > 0 && batch > lim / (rows * cols)))) return false;
+  return true;
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" {
+
+int64_t mxfp4_transposed_width(int64_t rows, int32_t E) {
+  if (rows < 0 || rows > (int64_t(1) << 31) || E < 0 || E > moe::kMaxGroups) return 0;
+  if (E == 0) return (rows + 31) / 32 * 32;
+  const int64_t a = moe::kGroupAlign;
+  return (rows + (a - 1) * E) / a * a;
+}
+
+moe_status mxfp4_quantize_transposed(const uint16_t* w_bf16, int64_t batch, int64_t rows,
+                                     int64_t cols, uint8_t* q_packed, uint8_t* scales,
+                                     int32_t* d_status, moe_stream stream) {
+  using namespace moe;
+  if (!sizes_ok(batch, rows, cols)) return MOE_ERR_SHAPE;
+  if (batch == 0 || rows == 0) return MOE_OK;
+  moe_status st = check(w_bf16, batch * rows, q_packed, scales, d_status);
+  if (st != MOE_OK) return st;
+  if ((st = check_device()) != MOE_OK) return st;
+  const int64_t P = mxfp4_transposed_width(rows, 0);
+  const int64_t tiles = batch * ((P + kRows - 1) / kRows) * ((cols + kCols - 1) / kCols);
+  return launch(quantize_transposed_kernel<false>, dim3(grid_for(tiles)), dim3(kThreads), 0,
+                static_cast<cudaStream_t>(stream), reinterpret_cast<const uint32_t*>(w_bf16), rows,
+                cols, batch, static_cast<const int32_t*>(nullptr), 0, P, q_packed, scales, d_status);
+}
+
+moe_status mxfp4_quantize_transposed_grouped(const uint16_t* w_bf16, int64_t rows, int64_t cols,
+                                             const int32_t* offsets, int32_t E, uint8_t* q_packed,
+                                             uint8_t* scales, int32_t* d_status,
+                                             moe_stream stream) {
+  using namespace moe;
+  if (!sizes_ok(1, rows, cols) || E < 1 || E > kMaxGroups) return MOE_ERR_SHAPE;
+  if (rows == 0) return MOE_OK;
+  const int64_t P = mxfp4_transposed_width(rows, E);
+  if (!offsets || !aligned16(offsets)) return MOE_ERR_INVALID_ARG;
+  moe_status st = check(w_bf16, rows, q_packed, scales, d_status);
+  if (st != MOE_OK) return st;
+  if ((st = check_device()) != MOE_OK) return st;
+  const int64_t tiles = (P / kRows) * ((cols + kCols - 1) / kCols);
+  return launch(quantize_transposed_kernel<true>, dim3(grid_for(tiles)), dim3(kThreads), 0,
+                static_cast<cudaStream_t>(stream), reinterpret_cast<const uint32_t*>(w_bf16), rows,
+                cols, int64_t(1), offsets, E, P, q_packed, scales, d_status);
+}
+
+}  // extern "C"

@@ -383,6 +383,30 @@ __device__ __forceinline__ void mma_mx_ss(uint32_t d_tmem, uint64_t a_desc, uint
       : "memory");
 }
 
+// Block-scaled MMA on packed E2M1 codes (two to a byte in shared memory), K = 64:
+//   D[M x N] (+)= sum over two 32-wide K blocks, each with its own scales, of
+//                 (A[m][k] * 2^(sa[m] - 127)) * (B[n][k] * 2^(sb[n] - 127))
+// E8M0 scale words in tensor memory as for mma_mx_ss; a word's four bytes are
+// the scales of 128 consecutive k, and `sf id` 0 or 2 picks its half.
+__device__ __forceinline__ void mma_mxf4_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate, uint32_t sfa_tmem,
+                                            uint32_t sfb_tmem) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], "
+      "p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(sfa_tmem), "r"(sfb_tmem)
+      : "memory");
+}
+
+// 32 rows x 16 bytes of shared memory -> 4 tensor-memory columns, repeated in
+// every lane quarter.  Ordered before later MMAs of the same thread.
+__device__ __forceinline__ void tmem_cp_32x128b(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+               : "memory");
+}
+
 // arrive once on `bar` when every tcgen05 operation this thread issued so far
 // has completed
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
@@ -406,6 +430,27 @@ __host__ __device__ constexpr uint32_t idesc_mx(uint32_t a_fmt, uint32_t b_fmt, 
 }
 __host__ __device__ constexpr uint32_t idesc_sf_ids(uint32_t a_id, uint32_t b_id) {
   return (b_id << 4) | (a_id << 29);
+}
+
+// Instruction descriptor of kind::mxf4 with E8M0 scales: both operands E2M1
+// (format 1 of this kind), K-major, fp32 accumulator, K = 64.
+__host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N) {
+  return (1u << 7)                                   // A format: E2M1
+         | (1u << 10)                                // B format: E2M1
+         | (static_cast<uint32_t>(N >> 3) << 17)     // N / 8
+         | (1u << 23)                                // scale format: E8M0
+         | (static_cast<uint32_t>(M >> 7) << 27);    // M / 128
+}
+
+// Shared-memory matrix descriptor of a 32-row x 16-byte block without swizzle
+// (row r at 16 r bytes; 8-row groups 128 bytes apart), for tmem_cp_32x128b.
+__device__ __forceinline__ uint64_t smem_desc_rows16(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);          // start address
+  d |= static_cast<uint64_t>(128u >> 4) << 16;                 // leading byte offset (unused)
+  d |= static_cast<uint64_t>(128u >> 4) << 32;                 // stride byte offset
+  d |= static_cast<uint64_t>(1u) << 46;                        // descriptor version
+  return d;
 }
 
 // Shared-memory matrix descriptor for a K-major operand stored as rows of
