@@ -20,17 +20,17 @@ __device__ __forceinline__ void group_rows(const int32_t* __restrict__ offsets, 
 
 // Exclusive prefix sums of units(e) over e in [0, E) into pfx[0..E] (shared
 // memory), by one whole warp; E <= kMaxGroups.
-template <typename Units>
-__device__ __forceinline__ void group_prefix(int E, int64_t* pfx, Units units) {
+template <typename Int, typename Units>
+__device__ __forceinline__ void group_prefix(int E, Int* pfx, Units units) {
   const int lane = threadIdx.x & 31;
-  int64_t carry = 0;
+  Int carry = 0;
   for (int e0 = 0; e0 < E; e0 += 32) {
     const int e = e0 + lane;
-    const int64_t n = e < E ? units(e) : 0;
-    int64_t incl = n;
+    const Int n = e < E ? units(e) : 0;
+    Int incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      const Int up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
       if (lane >= o) incl += up;
     }
     if (e < E) pfx[e] = carry + incl - n;

@@ -22,11 +22,11 @@
 //               NT x 128 bytes of A codes by TMA (zeros past the ends)
 //   warp 1      tensor-memory owner and MMA issuer; it also copies each stage's
 //               scale words from shared to tensor memory (tcgen05.cp)
-//   warps 2-5   scale loaders: E8M0 bytes from global memory, in chunks of 1024
-//               k (32 bytes of a row, one sector), laid down in shared memory in
-//               the order tcgen05.cp takes them
-//   warps 6-9   epilogue, one per lane quarter, from a double-buffered
-//               accumulator, so it overlaps the next tile's MMAs
+//   scale loaders (4 or 6 warps): E8M0 bytes from global memory, in chunks of
+//               1024 k (32 bytes of a row), laid down in shared memory in the
+//               order tcgen05.cp takes them
+//   epilogue (4 or 8 warps), one or two per lane quarter, from a
+//               double-buffered accumulator, so it overlaps the next tile's MMAs
 // Every wait is bounded (2 s); on expiry the kernel records MOE_ERR_TIMEOUT,
 // waits for its own copies and MMAs to finish and returns.
 #include <cuda.h>
@@ -47,36 +47,40 @@ constexpr int kStepsPerStage = 4;        // MMAs of 64 k per stage
 constexpr int kStagesPerChunk = 4;       // scale chunk: 1024 k, 8 words of 4 scales
 constexpr int kWords = 2 * kStagesPerChunk;
 constexpr int X_BYTES = BX * BKB;
-// one scale word of 128 rows: 512 bytes in tcgen05.cp's order, 16 apart so that
-// the loaders' stores of 8 words meet no bank conflict
-constexpr int kWordBytes = 512 + 16;
-constexpr int kThreads = 320;
-constexpr int kScaleWarps = 4, kEpiWarps = 4;
+constexpr int kWordBytes = 512;  // one scale word of 128 rows, in tcgen05.cp's order
+constexpr int kTableBytes = 3 * (kMaxGroups + 2) * 4;  // group table
 constexpr int kMaxStages = 8;
 constexpr int kChunkSlots = 2;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
+// Warps: producer, MMA issuer, scale loaders, epilogue.  The wide tiles, one
+// CTA per SM, take two warps of the epilogue per lane quarter.
+__host__ __device__ constexpr int y_blocks(int NT) { return (NT + 127) / 128; }
+__host__ __device__ constexpr int ctas_per_sm(int NT) { return NT <= 64 ? 2 : 1; }
+__host__ __device__ constexpr int scale_warps(int NT) { return 2 * (1 + y_blocks(NT)); }
+__host__ __device__ constexpr int epi_warps(int NT) { return NT > 64 ? 8 : 4; }
+__host__ __device__ constexpr int threads(int NT) {
+  return 32 * (2 + scale_warps(NT) + epi_warps(NT));
+}
+
 enum Mode : int { kDense = 0, kGrouped = 1, kWgrad = 2 };
 
-__host__ __device__ constexpr int y_blocks(int NT) { return (NT + 127) / 128; }
 __host__ __device__ constexpr int acc_cols(int NT) { return NT < 32 ? 32 : NT; }
 __host__ __device__ constexpr int sf_cols(int NT) { return 2 * 4 * (1 + y_blocks(NT)); }
 __host__ __device__ constexpr int tmem_cols(int NT) {
   const int need = 2 * acc_cols(NT) + 2 * sf_cols(NT);
   return need <= 128 ? 128 : (need <= 256 ? 256 : 512);
 }
-__host__ __device__ constexpr int ctas_per_sm(int NT) { return NT <= 64 ? 2 : 1; }
 __host__ __device__ constexpr int stage_bytes(int NT) { return X_BYTES + NT * BKB; }
 __host__ __device__ constexpr int chunk_bytes(int NT) { return kWords * (1 + y_blocks(NT)) * kWordBytes; }
 __host__ __device__ constexpr int stages(int NT) {
-  const int room = (ctas_per_sm(NT) == 2 ? 112 : 226) * 1024 - 1024 - 512 -
-                   (kMaxGroups + 1) * 8 - kChunkSlots * chunk_bytes(NT);
+  const int room = (ctas_per_sm(NT) == 2 ? 112 : 226) * 1024 - 1024 - 512 - kTableBytes -
+                   kChunkSlots * chunk_bytes(NT);
   const int n = room / stage_bytes(NT);
   return n < kMaxStages ? n : kMaxStages;
 }
 __host__ __device__ constexpr int smem_bytes(int NT) {
-  return 1024 + stages(NT) * stage_bytes(NT) + kChunkSlots * chunk_bytes(NT) +
-         (kMaxGroups + 1) * 8 + 512;
+  return 1024 + stages(NT) * stage_bytes(NT) + kChunkSlots * chunk_bytes(NT) + kTableBytes + 512;
 }
 
 struct Args {
@@ -88,20 +92,33 @@ struct Args {
   int64_t y_rows;          // rows of A
   int64_t x_total;         // rows of B over all groups
   int64_t K;               // contraction length (wgrad: its padded capacity)
-  int64_t S;               // wgrad: the capacity's last position / grouped: rows of A
+  int64_t S;               // bound of the offsets' values
   float alpha;
   void* out;
   int out_f32;
   int32_t* status;
 };
 
-// One output tile: B rows [x0, ..) of matrix xm, A rows [y0, y0 + ny), k in
-// [k0, k0 + 64 steps), out row y0 + i + yo.
+// One output tile: B rows [x0, ..) (of matrix e where B has groups), A rows
+// [y0, y0 + ny), k in [k0, k0 + 64 steps), first output row out_row.
 struct Work {
-  int64_t x0, y0, k0, out_row;
+  int64_t out_row;
+  int x0, y0, k0;
   int e, ny, steps;
-  bool live;
 };
+
+// Every group's first unit (tile of A rows, or 128 positions), first row and
+// rows, in shared memory.
+struct Groups {
+  int *pfx, *lo, *n;
+};
+
+// two fp32 -> bf16x2, round to nearest even (lo in the low half)
+__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 
 __device__ __forceinline__ void abort_cta(volatile int* abort, int32_t* status) {
   *abort = 1;
@@ -134,71 +151,164 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
 // Even split of n rows into tiles of at most NT: the width of each, a multiple
 // of 16 (the MMA's N step).
 template <int NT>
-__device__ __forceinline__ int tile_width(int64_t n) {
-  const int64_t t = (n + NT - 1) / NT;
-  return t == 0 ? 16 : static_cast<int>(((n + t - 1) / t + 15) / 16 * 16);
+__device__ __forceinline__ int tile_width(int n) {
+  const int t = (n + NT - 1) / NT;
+  return t == 0 ? 16 : ((n + t - 1) / t + 15) / 16 * 16;
 }
 
 // Tiles are numbered with the B side fastest, so the CTAs running at one time
-// share a few tiles of A rows.
+// share a few tiles of A rows.  `e` is the caller's cursor over the groups:
+// its tiles' numbers only rise.
 template <int NT>
-__device__ __forceinline__ Work work_of(const Args& a, const int64_t* pfx, int64_t xt, int64_t i) {
+__device__ __forceinline__ Work work_of(const Args& a, const Groups& g, uint32_t xt, uint32_t yt,
+                                        uint32_t i, int& e) {
   Work w;
-  w.x0 = i % xt * BX;
-  int64_t u = i / xt;
-  w.e = 0;
+  uint32_t u = i / xt;
+  w.x0 = static_cast<int>(i - u * xt) * BX;
   w.k0 = 0;
-  w.live = true;
-  int64_t lo = 0, n = a.y_rows;
   w.steps = static_cast<int>((a.K + 63) / 64);
+  int lo = 0, n = static_cast<int>(a.y_rows);
   if (a.mode == kGrouped) {
-    w.e = group_of(pfx, a.E, u);
-    u -= pfx[w.e];
-    int64_t hi;
-    group_rows(a.offsets, w.e, a.y_rows, lo, hi);
-    n = hi - lo;
+    while (static_cast<int>(u) >= g.pfx[e + 1]) ++e;
+    u -= g.pfx[e];
+    lo = g.lo[e];
+    n = g.n[e];
   } else if (a.mode == kWgrad) {
-    const int64_t yt = (a.y_rows + NT - 1) / NT;
-    w.e = static_cast<int>(u / yt);
-    u %= yt;
-    int64_t glo, ghi;
-    group_rows(a.offsets, w.e, a.S, glo, ghi);
-    w.k0 = pfx[w.e] * kGroupAlign;
+    e = static_cast<int>(u / yt);
+    u -= e * yt;
     // never past the capacity, whatever the offsets hold
-    const int64_t room = a.K - w.k0;
-    const int64_t len = room < 0 ? 0 : (ghi - glo < room ? ghi - glo : room);
+    const int64_t k0 = static_cast<int64_t>(g.pfx[e]) * kGroupAlign;
+    const int64_t room = a.K - k0;
+    const int64_t len = room < 0 ? 0 : (g.n[e] < room ? g.n[e] : room);
+    w.k0 = len > 0 ? static_cast<int>(k0) : 0;
     w.steps = static_cast<int>((len + 63) / 64);
   }
   const int width = tile_width<NT>(n);
-  w.y0 = lo + u * width;
-  const int64_t left = lo + n - w.y0;
-  w.ny = static_cast<int>(left < width ? (left < 0 ? 0 : left) : width);
-  w.out_row = w.y0 + (a.mode == kWgrad ? static_cast<int64_t>(w.e) * a.y_rows : 0);
+  w.e = e;
+  w.y0 = lo + static_cast<int>(u) * width;
+  w.ny = min(width, lo + n - w.y0);
+  w.out_row = w.y0 + (a.mode == kWgrad ? static_cast<int64_t>(e) * a.y_rows : 0);
   return w;
 }
 
-// Four scale bytes of a row from byte b of its ks; bytes past the row's end
-// read as 0 (their codes are zero).  `total` bounds the whole array.
-__device__ __forceinline__ uint32_t scale_word(const uint8_t* __restrict__ s, int64_t row_off,
-                                               int64_t b, int64_t ks, int64_t total) {
-  if (b >= ks) return 0u;
-  const int64_t at = row_off + b;
-  uint32_t v;
-  if ((ks & 3) == 0) {
-    v = __ldg(reinterpret_cast<const uint32_t*>(s + at));
-  } else if (at + 8 <= total) {
-    const uint32_t* p = reinterpret_cast<const uint32_t*>(s + (at & ~int64_t(3)));
-    v = __funnelshift_r(__ldg(p), __ldg(p + 1), static_cast<uint32_t>(at & 3) * 8);
-  } else {
-    v = 0;
-    for (int i = 0; i < 4 && at + i < total; ++i) v |= static_cast<uint32_t>(__ldg(s + at + i)) << (8 * i);
+// 32 scale bytes (a chunk of a row) from address p of an array that ends at
+// `end`, as eight words; bytes from `n` on read as 0 (their codes are zero).
+// Rows start at any byte, so the chunk is read as the three aligned 16-byte
+// pieces that cover it and shifted into place.
+struct Pieces {
+  uint4 v[3];
+};
+
+__device__ __forceinline__ bool past_end(const uint8_t* p, int n, const uint8_t* end) {
+  const uint8_t* last = p + n - 1;  // the piece of the last byte ends behind the array
+  return n > 0 && last - (reinterpret_cast<uintptr_t>(last) & 15u) + 16 > end;
+}
+
+__device__ __forceinline__ Pieces load_pieces(const uint8_t* p, int n, const uint8_t* end) {
+  const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u);
+  const uint4* a0 = reinterpret_cast<const uint4*>(p - mis);
+  const bool all = !past_end(p, n, end);
+  Pieces r;
+#pragma unroll
+  for (int j = 0; j < 3; ++j)
+    r.v[j] = all && n > 0 && 16 * j < mis + n ? __ldg(a0 + j) : make_uint4(0u, 0u, 0u, 0u);
+  return r;
+}
+
+__device__ __noinline__ void load_bytes(const uint8_t* p, int n, uint32_t (&w)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    w[i] = 0u;
+    for (int j = 4 * i; j < n && j < 4 * i + 4; ++j)
+      w[i] |= static_cast<uint32_t>(__ldg(p + j)) << (8 * (j & 3));
   }
-  const int64_t left = ks - b;
-  return left < 4 ? v & ((1u << (8 * left)) - 1u) : v;
+}
+
+__device__ __forceinline__ void align_words(const Pieces& r, const uint8_t* p, int n, uint32_t (&w)[8]) {
+  uint32_t x[12];
+#pragma unroll
+  for (int j = 0; j < 3; ++j) {
+    x[4 * j] = r.v[j].x;
+    x[4 * j + 1] = r.v[j].y;
+    x[4 * j + 2] = r.v[j].z;
+    x[4 * j + 3] = r.v[j].w;
+  }
+  const uint32_t mis = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15u);
+#pragma unroll
+  for (int i = 0; i < 11; ++i) x[i] = mis & 4u ? x[i + 1] : x[i];
+#pragma unroll
+  for (int i = 0; i < 9; ++i) x[i] = mis & 8u ? x[i + 2] : x[i];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = __funnelshift_r(x[i], x[i + 1], (mis & 3u) * 8);
+  if (n < 32) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int left = n - 4 * i;
+      if (left < 4) w[i] = left > 0 ? w[i] & ((1u << (8 * left)) - 1u) : 0u;
+    }
+  }
+}
+
+// 16 accumulator columns (output rows row0 + c, c < ny - c0) of this lane's
+// output column n, times alpha, into out.
+template <bool F32>
+__device__ __forceinline__ void store16(const uint32_t (&r)[16], float alpha, void* out, int64_t row,
+                                        int64_t ld, int64_t n, bool live, int ny) {
+  if (F32) {
+    float* p = static_cast<float*>(out) + row * ld + n;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      if (live && k < ny) *p = alpha * __uint_as_float(r[k]);
+      p += ld;
+    }
+  } else if ((ld & 1) == 0) {
+    // neighbouring lanes swap halves of a column pair, so each stores two
+    // output columns of one row: half the stores
+    const int odd = threadIdx.x & 1;
+    uint16_t* p = static_cast<uint16_t*>(out) + (row + odd) * ld + (n - odd);
+#pragma unroll
+    for (int k = 0; k < 16; k += 2) {
+      const float v0 = alpha * __uint_as_float(r[k]), v1 = alpha * __uint_as_float(r[k + 1]);
+      const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? v0 : v1, 1);
+      const uint32_t packed = odd ? cvt_bf16x2(got, v1) : cvt_bf16x2(v0, got);
+      if (live && k + odd < ny) *reinterpret_cast<uint32_t*>(p) = packed;
+      p += 2 * ld;
+    }
+  } else {
+    uint16_t* p = static_cast<uint16_t*>(out) + row * ld + n;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const float v = alpha * __uint_as_float(r[k]);
+      if (live && k < ny) *p = static_cast<uint16_t>(cvt_bf16x2(v, v));
+      p += ld;
+    }
+  }
+}
+
+// Columns [c0, c1) of a tile's accumulator (a multiple of 16 of them, the last
+// ones possibly past its ny rows).
+template <bool F32>
+__device__ __forceinline__ void store_columns(uint32_t acc, const Args& a, const Work& w, int64_t n,
+                                              int c0, int c1) {
+  const bool live = n < a.x_rows;
+  for (int c = c0; c < c1; c += 32) {
+    uint32_t r[2][16];
+    const bool two = c + 16 < c1;
+    if (w.steps > 0) {
+      tc::tmem_ld16(acc + c, r[0]);
+      if (two) tc::tmem_ld16(acc + c + 16, r[1]);
+      tc::tmem_ld_wait();
+    } else {
+#pragma unroll
+      for (int k = 0; k < 16; ++k) r[0][k] = r[1][k] = 0u;  // an empty sum
+    }
+    store16<F32>(r[0], a.alpha, a.out, w.out_row + c, a.x_rows, n, live, w.ny - c);
+    if (two) store16<F32>(r[1], a.alpha, a.out, w.out_row + c + 16, a.x_rows, n, live, w.ny - c - 16);
+  }
 }
 
 template <int NT>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
+__global__ void __launch_bounds__(threads(NT), ctas_per_sm(NT))
     mxfp4_matmul_kernel(const __grid_constant__ CUtensorMap map_x,
                         const __grid_constant__ CUtensorMap map_y, const Args a) {
   constexpr int NS = stages(NT), STAGE = stage_bytes(NT), YB = y_blocks(NT);
@@ -207,8 +317,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* chunks = smem + NS * STAGE;
-  int64_t* pfx = reinterpret_cast<int64_t*>(chunks + kChunkSlots * chunk_bytes(NT));
-  uint64_t* full = reinterpret_cast<uint64_t*>(pfx + kMaxGroups + 1);  // [NS] stage copies landed
+  constexpr int kEpi = epi_warps(NT), kEpi0 = 2 + scale_warps(NT);
+  Groups grp;
+  grp.pfx = reinterpret_cast<int*>(chunks + kChunkSlots * chunk_bytes(NT));
+  grp.lo = grp.pfx + kMaxGroups + 2;
+  grp.n = grp.lo + kMaxGroups + 2;
+  uint64_t* full = reinterpret_cast<uint64_t*>(grp.n + kMaxGroups + 2);  // [NS] stage copies landed
   uint64_t* empty = full + kMaxStages;     // [NS] stage MMAs complete
   uint64_t* sfull = empty + kMaxStages;    // [2] scale chunk written
   uint64_t* sempty = sfull + kChunkSlots;  // [2] scale chunk read
@@ -225,12 +339,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
       tc::mbar_init(&empty[s], 1);
     }
     for (int s = 0; s < kChunkSlots; ++s) {
-      tc::mbar_init(&sfull[s], kScaleWarps);
+      tc::mbar_init(&sfull[s], 1 + YB);
       tc::mbar_init(&sempty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(&dfull[b], 1);
-      tc::mbar_init(&dempty[b], kEpiWarps);
+      tc::mbar_init(&dempty[b], kEpi);
     }
     tc::mbar_init(drain, 1);
     *abort_flag = 0;
@@ -243,83 +357,85 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
     tc::tmem_relinquish();
   }
   if (warp == 2 && a.mode != kDense)
-    group_prefix(a.E, pfx, [&](int e) {
+    group_prefix(a.E, grp.pfx, [&](int e) {
       int64_t lo, hi;
-      group_rows(a.offsets, e, a.mode == kGrouped ? a.y_rows : a.S, lo, hi);
-      return a.mode == kGrouped ? (hi - lo + NT - 1) / NT
-                                : (hi - lo + kGroupAlign - 1) / kGroupAlign;
+      group_rows(a.offsets, e, a.S, lo, hi);
+      const int n = static_cast<int>(hi - lo);
+      grp.lo[e] = static_cast<int>(lo);
+      grp.n[e] = n;
+      return a.mode == kGrouped ? (n + NT - 1) / NT : (n + kGroupAlign - 1) / kGroupAlign;
     });
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  const int64_t xt = (a.x_rows + BX - 1) / BX;
-  const int64_t yt = (a.y_rows + NT - 1) / NT;
-  const int64_t n_work =
-      xt * (a.mode == kDense ? yt : (a.mode == kGrouped ? pfx[a.E] : yt * a.E));
-  const int64_t ks = a.K / 32;
+  const uint32_t xt = static_cast<uint32_t>((a.x_rows + BX - 1) / BX);
+  const uint32_t yt = static_cast<uint32_t>((a.y_rows + NT - 1) / NT);
+  const uint32_t n_work =
+      xt * (a.mode == kDense ? yt : (a.mode == kGrouped ? grp.pfx[a.E] : yt * a.E));
+  const int ks = static_cast<int>(a.K / 32);
+  int ge = 0;  // this role's cursor over the groups
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      int64_t g = 0;
+      uint32_t g = 0;
       bool ok = true;
-      for (int64_t i = blockIdx.x; ok && i < n_work; i += gridDim.x) {
-        const Work w = work_of<NT>(a, pfx, xt, i);
+      for (uint32_t i = blockIdx.x; ok && i < n_work; i += gridDim.x) {
+        const Work w = work_of<NT>(a, grp, xt, yt, i, ge);
         const int nst = (w.steps + kStepsPerStage - 1) / kStepsPerStage;
         for (int st = 0; st < nst; ++st, ++g) {
-          const int s = static_cast<int>(g % NS);
-          const int64_t n = g / NS;
+          const uint32_t s = g % NS, n = g / NS;
           if (n > 0 && !wait1(&empty[s], (n - 1) & 1, abort_flag, a.status)) {
             ok = false;
             break;
           }
           uint8_t* dst = smem + s * STAGE;
-          const int kb = static_cast<int>(w.k0 / 2) + st * BKB;
+          const int kb = w.k0 / 2 + st * BKB;
           tc::mbar_arrive_expect_tx(&full[s], STAGE);
-          tc::tma_load_3d(dst, &map_x, &full[s], kb, static_cast<int>(w.x0),
+          tc::tma_load_3d(dst, &map_x, &full[s], kb, w.x0,
                           a.mode == kGrouped ? w.e : 0);
-          tc::tma_load_2d(dst + X_BYTES, &map_y, &full[s], kb, static_cast<int>(w.y0));
+          tc::tma_load_2d(dst + X_BYTES, &map_y, &full[s], kb, w.y0);
         }
       }
       // every copy this thread issued has landed before the CTA exits
-      for (int64_t i = g > NS ? g - NS : 0; i < g; ++i)
+      for (uint32_t i = g > NS ? g - NS : 0; i < g; ++i)
         tc::mbar_drain(&full[i % NS], (i / NS) & 1, kWaitLimitNs / 8);
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
     if (lane == 0) {
-      int64_t g = 0, ch = 0, it = 0;
+      uint32_t g = 0, ch = 0, it = 0;
       bool ok = true;
-      for (int64_t i = blockIdx.x; ok && i < n_work; i += gridDim.x, ++it) {
-        const Work w = work_of<NT>(a, pfx, xt, i);
+      for (uint32_t i = blockIdx.x; ok && i < n_work; i += gridDim.x, ++it) {
+        const Work w = work_of<NT>(a, grp, xt, yt, i, ge);
         const uint32_t idesc = tc::idesc_mxf4(BX, (w.ny + 15) & ~15);
-        const uint32_t d = tmem + static_cast<uint32_t>(it & 1) * ACC;
+        const uint32_t d = tmem + (it & 1) * ACC;
         // accumulator it & 1 was last used by tile it - 2
         if (it >= 2 && !wait1(&dempty[it & 1], ((it >> 1) - 1) & 1, abort_flag, a.status)) break;
         const int nst = (w.steps + kStepsPerStage - 1) / kStepsPerStage;
         for (int st = 0; st < nst; ++st, ++g) {
           const int cw = st % kStagesPerChunk;
-          const int cs = static_cast<int>(ch % kChunkSlots);
+          const uint32_t cs = ch % kChunkSlots;
           if (cw == 0 && !wait1(&sfull[cs], (ch / kChunkSlots) & 1, abort_flag, a.status)) {
             ok = false;
             break;
           }
           // the tensor-memory scale columns of stage g were last read by stage g - 2
           if (g >= 2) {
-            const int64_t p = g - 2;
+            const uint32_t p = g - 2;
             if (!wait1(&empty[p % NS], (p / NS) & 1, abort_flag, a.status)) {
               ok = false;
               break;
             }
           }
-          const int s = static_cast<int>(g % NS);
+          const uint32_t s = g % NS;
           if (!wait1(&full[s], (g / NS) & 1, abort_flag, a.status)) {
             ok = false;
             break;
           }
           tc::tc_fence_after();
-          const uint32_t sf = tmem + 2 * ACC + static_cast<uint32_t>(g & 1) * SF;
+          const uint32_t sf = tmem + 2 * ACC + (g & 1) * SF;
           const uint32_t chunk = tc::smem_u32(chunks + cs * chunk_bytes(NT));
           // columns: [word 0: X, Y blocks][word 1: X, Y blocks], 4 columns a block
 #pragma unroll
@@ -353,46 +469,54 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
       else
         tc::mbar_arrive(drain);
     }
-  } else if (warp < 2 + kScaleWarps) {
+  } else if (warp < kEpi0) {
     // -------------------------------------------------------- scale loaders
-    // Lane (word w = lane % 8, quarter c = lane / 8) carries word w of rows
-    // 32 c + rr: 8 neighbouring lanes read 32 contiguous bytes of a row.
-    const int wi = warp - 2, kw = lane & 7, c = lane >> 3;
-    const int64_t x_bytes = a.x_total * ks, y_bytes = a.y_rows * ks;
-    int64_t ch = 0;
+    // One warp per block of 128 rows (B's, then A's): lane l carries the 32
+    // bytes of the chunk of rows l, l + 32, l + 64 and l + 96, which are the 16
+    // bytes of row l of tcgen05.cp's order for each of the 8 words.  Two groups
+    // of warps take every second chunk each, so one's loads are in flight while
+    // the other's chunk is used.
+    const uint32_t mine = static_cast<uint32_t>(warp - 2) / (1 + YB);
+    const int blk = (warp - 2) % (1 + YB);
+    const uint8_t* all = blk == 0 ? a.xs : a.ys;
+    const uint8_t* end = all + (blk == 0 ? a.x_total : a.y_rows) * ks;
+    uint32_t ch = 0;
     bool ok = true;
-    for (int64_t i = blockIdx.x; ok && i < n_work; i += gridDim.x) {
-      const Work w = work_of<NT>(a, pfx, xt, i);
+    for (uint32_t i = blockIdx.x; ok && i < n_work; i += gridDim.x) {
+      const Work w = work_of<NT>(a, grp, xt, yt, i, ge);
       const int nst = (w.steps + kStepsPerStage - 1) / kStepsPerStage;
       const int nch = (nst + kStagesPerChunk - 1) / kStagesPerChunk;
-      const int64_t xrow = w.x0 + (a.mode == kGrouped ? static_cast<int64_t>(w.e) * a.x_rows : 0);
+      const int64_t row0 = blk == 0 ? w.x0 + (a.mode == kGrouped ? w.e * a.x_rows : 0)
+                                    : static_cast<int64_t>(w.y0) + (blk - 1) * 128;
+      const int rows = blk == 0 ? static_cast<int>(min(a.x_rows - w.x0, static_cast<int64_t>(BX)))
+                                : w.ny - (blk - 1) * 128;
+      const uint8_t* base = all + (row0 + lane) * ks + w.k0 / 32;
+      const int left = ks - w.k0 / 32;
       for (int q = 0; q < nch; ++q, ++ch) {
-        const int64_t byte = w.k0 / 32 + (static_cast<int64_t>(q) * kWords + kw) * 4;
-        uint32_t v[8 * (1 + YB)];
+        if ((ch & 1) != mine) continue;
+        const int byte = q * kWords * 4;
+        const uint8_t* p = base + byte;
+        const int n = min(32, left - byte);
+        Pieces raw[4];
 #pragma unroll
-        for (int b = 0; b < 1 + YB; ++b)
+        for (int c = 0; c < 4; ++c)
+          raw[c] = load_pieces(p + c * 32 * ks, lane + 32 * c < rows ? n : 0, end);
+        uint32_t v[4][8];
 #pragma unroll
-          for (int r = 0; r < 8; ++r) {
-            const int row = (b > 0 ? b - 1 : 0) * 128 + c * 32 + wi + 4 * r;
-            const bool in = b == 0 ? w.x0 + row < a.x_rows : row < w.ny;
-            v[b * 8 + r] = !in ? 0u
-                           : b == 0
-                               ? scale_word(a.xs, (xrow + row) * ks, byte, ks, x_bytes)
-                               : scale_word(a.ys, (w.y0 + row) * ks, byte, ks, y_bytes);
-          }
-        const int cs = static_cast<int>(ch % kChunkSlots);
-        const int64_t n = ch / kChunkSlots;
-        if (n > 0 && !warp_wait(&sempty[cs], (n - 1) & 1, abort_flag, a.status)) {
+        for (int c = 0; c < 4; ++c) {
+          const int nr = lane + 32 * c < rows ? n : 0;
+          align_words(raw[c], p + c * 32 * ks, nr, v[c]);
+          if (past_end(p + c * 32 * ks, nr, end)) load_bytes(p + c * 32 * ks, nr, v[c]);
+        }
+        const uint32_t cs = ch % kChunkSlots, use = ch / kChunkSlots;
+        if (use > 0 && !warp_wait(&sempty[cs], (use - 1) & 1, abort_flag, a.status)) {
           ok = false;
           break;
         }
-        uint8_t* chunk = chunks + cs * chunk_bytes(NT);
+        uint8_t* dst = chunks + cs * chunk_bytes(NT) + blk * kWords * kWordBytes + lane * 16;
 #pragma unroll
-        for (int b = 0; b < 1 + YB; ++b)
-#pragma unroll
-          for (int r = 0; r < 8; ++r)
-            *reinterpret_cast<uint32_t*>(chunk + (b * kWords + kw) * kWordBytes +
-                                         (wi + 4 * r) * 16 + c * 4) = v[b * 8 + r];
+        for (int k = 0; k < kWords; ++k)
+          *reinterpret_cast<uint4*>(dst + k * kWordBytes) = make_uint4(v[0][k], v[1][k], v[2][k], v[3][k]);
         // the tensor core's copy reads shared memory through the async proxy
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
@@ -402,37 +526,24 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT))
   } else {
     // ------------------------------------------------------------- epilogue
     const int q = warp & 3;  // the lane quarter this warp may read
+    const int part = (warp - kEpi0) >> 2;
     const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
-    int64_t it = 0;
-    for (int64_t i = blockIdx.x; i < n_work; i += gridDim.x, ++it) {
-      const Work w = work_of<NT>(a, pfx, xt, i);
-      const int b = static_cast<int>(it & 1);
+    uint32_t it = 0;
+    for (uint32_t i = blockIdx.x; i < n_work; i += gridDim.x, ++it) {
+      const Work w = work_of<NT>(a, grp, xt, yt, i, ge);
+      const uint32_t b = it & 1;
       if (!warp_wait(&dfull[b], (it >> 1) & 1, abort_flag, a.status)) break;
       tc::tc_fence_after();
-      const int64_t n = w.x0 + q * 32 + lane;
-      const bool live = n < a.x_rows;
-      const uint32_t acc = tmem + static_cast<uint32_t>(b) * ACC + lane_base;
-      for (int c = 0; c < w.ny; c += 16) {
-        uint32_t r[16];
-        if (w.steps > 0) {
-          tc::tmem_ld16(acc + c, r);
-          tc::tmem_ld_wait();
-        } else {
-#pragma unroll
-          for (int k = 0; k < 16; ++k) r[k] = 0u;  // an empty sum
-        }
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float v = a.alpha * __uint_as_float(r[k]);
-          if (live && c + k < w.ny) {
-            const int64_t at = (w.out_row + c + k) * a.x_rows + n;
-            if (a.out_f32)
-              static_cast<float*>(a.out)[at] = v;
-            else
-              static_cast<uint16_t*>(a.out)[at] = f32_to_bf16_rne(v);
-          }
-        }
-      }
+      const int64_t n = static_cast<int64_t>(w.x0) + q * 32 + lane;
+      const uint32_t acc = tmem + b * ACC + lane_base;
+      // the tile's columns, split over this quarter's warps in steps of 32
+      const int all = (w.ny + 15) & ~15;
+      const int half = kEpi == 8 ? (all / 2 + 31) & ~31 : all;
+      const int c0 = part ? min(half, all) : 0, c1 = part ? all : min(half, all);
+      if (a.out_f32)
+        store_columns<true>(acc, a, w, n, c0, c1);
+      else
+        store_columns<false>(acc, a, w, n, c0, c1);
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&dempty[b]);
@@ -492,7 +603,7 @@ moe_status launch_nt(const Args& a, const uint8_t* xq, const uint8_t* yq, int64_
   if (!encode(&mx, 3, xq, xd, xs, xb) || !encode(&my, 2, yq, yd, ys, yb)) return MOE_ERR_CUDA;
   const int64_t cap = static_cast<int64_t>(sm_count()) * ctas_per_sm(NT);
   const dim3 grid(static_cast<unsigned>(max_work < cap ? max_work : cap));
-  return launch(mxfp4_matmul_kernel<NT>, grid, dim3(kThreads), smem_bytes(NT), stream, mx, my, a);
+  return launch(mxfp4_matmul_kernel<NT>, grid, dim3(threads(NT)), smem_bytes(NT), stream, mx, my, a);
 }
 
 // Rows of A per tile: `rows` is what one tile may meet, twice the mean of a
@@ -618,7 +729,7 @@ moe_status mxfp4_matmul_grouped_wgrad(const uint8_t* a_q, const uint8_t* a_s, co
   a.x_rows = a.x_total = N;
   a.y_rows = M;
   a.K = P;
-  a.S = int64_t(1) << 31;
+  a.S = P;  // a group never has more rows than positions
   a.alpha = alpha;
   a.out = out;
   a.out_f32 = out_type == MOE_OUT_FP32;
