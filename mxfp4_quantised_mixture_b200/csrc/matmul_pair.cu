@@ -1,0 +1,400 @@
+// The MXFP4 products on CTA pairs: tiles of 256 rows of B by up to 192 rows of A.
+//
+// "MXFP4-based MoE technical review", section 2 (MXFP4 training).  The same
+// products as csrc/matmul.cu, for more than 128 rows of A.
+//
+// What bounds a 4-bit product is not the tensor core but what feeds it: 64 k of
+// a 128 x 224 tile take the tensor core 112 cycles and move 11 KB into and out
+// of shared memory, 196 bytes a cycle where an SM has 128.  A pair of SMs
+// (cta_group::2, M = 256) holds 128 rows of B and half of the A rows in each,
+// so the same 112 cycles per SM move 7.5 KB.
+//
+// The tensor core takes the block scales from tensor memory.  tcgen05.cp runs
+// in the MMAs' own pipe and cost 240 ns of every stage's 450 (measured on the
+// one-CTA form of this kernel); here four warps write them with tcgen05.st
+// beside the MMAs, two stages deep.
+//
+// Warp roles, in each CTA of the pair:
+//   warp 0       producer: per stage of 512 k its own 128 rows of B and its half
+//                of the A rows, by TMA into its own shared memory
+//   warp 1       tensor-memory owner; in the first CTA the MMA issuer, in the
+//                second it tells the issuer that a stage's codes have landed
+//   warps 2-7    scale loaders: one per 128-row block (B, A, A), in two groups
+//                that take every second chunk of 1024 k
+//   warps 8-11   scale writers, one per lane quarter: a stage's words from shared
+//                to tensor memory, and the issuer told
+//   warps 12-19  epilogue, two per lane quarter, from a double-buffered
+//                accumulator
+// The issuer's commits reach both CTAs' barriers.  Every wait is bounded (2 s);
+// on expiry the kernel records MOE_ERR_TIMEOUT, waits for its own copies and
+// MMAs to finish and returns.  Copies are always local to a CTA and awaited by
+// it; the CTAs of a pair leave together.
+#include <cuda.h>
+
+#include <atomic>
+
+#include "matmul_common.cuh"
+
+namespace moe {
+namespace {
+
+using namespace mm;
+
+constexpr int NT = 192;    // rows of A per tile
+constexpr int STEP = 32;   // in steps of the pair's N
+constexpr int BX = 256;    // rows of B per tile
+constexpr int YB = 2;      // 128-row blocks of A's scales
+constexpr int X_BYTES = 128 * BKB, Y_BYTES = NT / 2 * BKB, WINDOW = X_BYTES + Y_BYTES;
+constexpr int WPS = 2;                     // windows of 256 k per stage
+constexpr int STAGE = WPS * WINDOW;
+constexpr int STEPS = WPS * kStepsPerStage;  // MMAs of 64 k per stage
+constexpr int SPC = kStagesPerChunk / WPS;   // stages per scale chunk
+constexpr int kLoaders = 2 * (1 + YB), kWriters = 4, kEpi = 8;
+constexpr int kWriter0 = 2 + kLoaders, kEpi0 = kWriter0 + kWriters;
+constexpr int kThreads = 32 * (kEpi0 + kEpi);
+constexpr int kChunkBytes = (1 + YB) * kWords * kWordBytes;
+constexpr int SFW = 4 * (1 + YB);      // scale columns of one word (128 k)
+constexpr int SF = 2 * WPS * SFW;      // of a stage
+constexpr int TMEM = 512;
+constexpr int SLOTS = 2;               // stages of scales in tensor memory
+static_assert(2 * NT + SLOTS * SF <= TMEM, "two accumulators and the scale slots");
+constexpr int NS = 3;  // copy ring
+static_assert(SLOTS <= NS, "a slot's last stage is found by its ring barrier");
+constexpr int kSmem = 1024 + NS * STAGE + kChunkSlots * kChunkBytes + kTableBytes + 512;
+static_assert(NS <= kMaxStages && kSmem <= 227 * 1024, "shared memory");
+
+__device__ __forceinline__ int pair_stages(const Work& w) { return (w.steps + STEPS - 1) / STEPS; }
+
+// Lane 0 waits for a phase (its own sleep short), the warp follows.
+__device__ __forceinline__ bool lead_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                          int32_t* status) {
+  bool r = true;
+  if ((threadIdx.x & 31) == 0) r = tc::mbar_wait_sleep(bar, parity, abort, kWaitLimitNs, 20);
+  r = __shfl_sync(0xFFFFFFFFu, r, 0);
+  if (!r) abort_cta(abort, status);
+  return r;
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    mxfp4_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_x,
+                             const __grid_constant__ CUtensorMap map_y, const Args a) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* chunks = smem + NS * STAGE;
+  Groups grp;
+  grp.pfx = reinterpret_cast<int*>(chunks + kChunkSlots * kChunkBytes);
+  grp.lo = grp.pfx + kMaxGroups + 2;
+  grp.n = grp.lo + kMaxGroups + 2;
+  uint64_t* full = reinterpret_cast<uint64_t*>(grp.n + kMaxGroups + 2);  // [NS] own copies landed
+  uint64_t* ready = full + kMaxStages;     // [NS] both CTAs' codes and scales (first CTA)
+  uint64_t* empty = ready + kMaxStages;    // [NS] stage MMAs complete
+  uint64_t* sfull = empty + kMaxStages;    // [2] scale chunk in shared memory
+  uint64_t* sempty = sfull + kChunkSlots;  // [2] scale chunk read
+  uint64_t* dfull = sempty + kChunkSlots;  // [2] accumulator complete
+  uint64_t* dempty = dfull + 2;            // [2] accumulator read by both CTAs (first CTA)
+  uint64_t* drain = dempty + 2;            // every MMA issued has completed
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(tc::cluster_rank());
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      tc::mbar_init(&full[s], 1);
+      tc::mbar_init(&ready[s], 2 * kWriters + 1);
+      tc::mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < kChunkSlots; ++s) {
+      tc::mbar_init(&sfull[s], 1 + YB);
+      tc::mbar_init(&sempty[s], kWriters);
+    }
+    for (int b = 0; b < 2; ++b) {
+      tc::mbar_init(&dfull[b], 1);
+      tc::mbar_init(&dempty[b], 2 * kEpi);
+    }
+    tc::mbar_init(drain, 1);
+    *abort_flag = 0;
+    tc::fence_mbar_init();
+    tc::tma_prefetch_desc(&map_x);
+    tc::tma_prefetch_desc(&map_y);
+  }
+  if (warp == 1) {
+    tc::tmem_alloc_pair(tmem_holder, TMEM);
+    tc::tmem_relinquish_pair();
+  }
+  if (warp == 2 && a.mode != kDense) fill_groups<NT>(a, grp);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::cluster_sync();  // both CTAs' barriers exist before either is told anything
+  tc::tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const uint32_t xt = static_cast<uint32_t>((a.x_rows + BX - 1) / BX);
+  const uint32_t yt = static_cast<uint32_t>((a.y_rows + NT - 1) / NT);
+  const uint32_t n_work = tiles(a, grp, xt, yt);
+  const uint32_t first = blockIdx.x >> 1, stride = gridDim.x >> 1;
+  const int ks = static_cast<int>(a.K / 32);
+  int ge = 0;  // this role's cursor over the groups
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    uint32_t s = 0, phase = 0, issued = 0;
+    bool ok = true;
+    for (uint32_t i = first; ok && i < n_work; i += stride) {
+      const Work w = work_of<NT, STEP, BX>(a, grp, xt, yt, i, ge);
+      const int nst = pair_stages(w), half = ((w.ny + STEP - 1) & ~(STEP - 1)) / 2;
+      for (int st = 0; st < nst; ++st) {
+        if (issued >= NS && !all_wait(&empty[s], phase ^ 1u, abort_flag, a.status)) {
+          ok = false;
+          break;
+        }
+        if (tc::elect_one()) {
+          const int nw = min(WPS, stages_of(w) - st * WPS);
+          tc::mbar_arrive_expect_tx(&full[s], nw * WINDOW);
+#pragma unroll
+          for (int v = 0; v < WPS; ++v) {
+            if (v >= nw) break;
+            uint8_t* dst = smem + s * STAGE + v * WINDOW;
+            const int kb = w.k0 / 2 + (st * WPS + v) * BKB;
+            tc::tma_load_3d(dst, &map_x, &full[s], kb, w.x0 + rank * 128, a.mode == kGrouped ? w.e : 0);
+            tc::tma_load_3d(dst + X_BYTES, &map_y, &full[s], kb, w.y0 + rank * half, 0);
+          }
+        }
+        __syncwarp();
+        ++issued;
+        if (++s == NS) {
+          s = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    // every copy this warp issued has landed before the CTA exits
+    for (uint32_t i = issued > NS ? issued - NS : 0; i < issued; ++i)
+      tc::mbar_drain(&full[i % NS], (i / NS) & 1, kWaitLimitNs / 8);
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMA issuer
+    if (rank == 0) {
+      const uint64_t desc0 = tc::smem_desc_sw128(tc::smem_u32(smem));
+      uint32_t it = 0, s = 0, phase = 0, slot = 0;
+      bool ok = true, any = false;
+      for (uint32_t i = first; ok && i < n_work; i += stride, ++it) {
+        const Work w = work_of<NT, STEP, BX>(a, grp, xt, yt, i, ge);
+        const uint32_t idesc = tc::idesc_mxf4(BX, (w.ny + STEP - 1) & ~(STEP - 1));
+        const uint32_t d = tmem + (it & 1) * NT;
+        // accumulator it & 1 was last used by tile it - 2
+        if (it >= 2 && !all_wait(&dempty[it & 1], ((it >> 1) - 1) & 1, abort_flag, a.status)) break;
+        const int nst = pair_stages(w);
+        for (int st = 0; st < nst; ++st) {
+          // its own codes, then the other CTA's and both CTAs' scales
+          if (!all_wait(&full[s], phase, abort_flag, a.status) ||
+              !all_wait(&ready[s], phase, abort_flag, a.status)) {
+            ok = false;
+            break;
+          }
+          tc::tc_fence_after();
+          const uint32_t sf = tmem + 2 * NT + slot * SF;
+          // a descriptor addresses shared memory in 16-byte units
+          const uint64_t xd = desc0 + s * (STAGE / 16);
+          const int left = w.steps - st * STEPS;
+          if (tc::elect_one()) {
+#pragma unroll
+            for (int k = 0; k < STEPS; ++k) {
+              if (k >= left) break;
+              const uint32_t sx = sf + (k >> 1) * SFW, id = (k & 1) * 2;
+              const uint64_t xk = xd + (k / kStepsPerStage) * (WINDOW / 16) + 2 * (k % kStepsPerStage);
+              tc::mma_mxf4_pair(d, xk, xk + X_BYTES / 16, idesc | tc::idesc_sf_ids(id, id),
+                                (st | k) != 0 ? 1u : 0u, sx, sx + 4);
+            }
+            tc::mma_commit_pair(&empty[s]);
+            if (st == nst - 1) tc::mma_commit_pair(&dfull[it & 1]);
+          }
+          __syncwarp();
+          any = true;
+          if (++s == NS) {
+            s = 0;
+            phase ^= 1u;
+          }
+          if (++slot == SLOTS) slot = 0;
+        }
+        // an empty sum: its zeros wait for nothing
+        if (nst == 0 && tc::elect_one()) tc::mma_commit_pair(&dfull[it & 1]);
+        any |= nst == 0;
+        __syncwarp();
+      }
+      // completes, in both CTAs, once every operation this warp issued has finished
+      if (tc::elect_one()) {
+        if (any) {
+          tc::mma_commit_pair(drain);
+        } else {
+          tc::mbar_arrive(drain);
+          tc::mbar_arrive_cluster(tc::cluster_addr(drain, 1));
+        }
+      }
+    } else {
+      // the second CTA: its codes' arrival, passed on to the issuer
+      const uint32_t to = tc::cluster_addr(ready, 0);
+      uint32_t s = 0, phase = 0;
+      bool ok = true;
+      for (uint32_t i = first; ok && i < n_work; i += stride) {
+        const int nst = pair_stages(work_of<NT, STEP, BX>(a, grp, xt, yt, i, ge));
+        for (int st = 0; ok && st < nst; ++st) {
+          ok = all_wait(&full[s], phase, abort_flag, a.status);
+          if (ok && lane == 0) tc::mbar_arrive_cluster(to + s * 8);
+          if (++s == NS) {
+            s = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    }
+  } else if (warp < kWriter0) {
+    // -------------------------------------------------------- scale loaders
+    const uint32_t mine = static_cast<uint32_t>(warp - 2) / (1 + YB);
+    const int blk = (warp - 2) % (1 + YB);
+    uint32_t ch = 0;
+    bool ok = true;
+    for (uint32_t i = first; ok && i < n_work; i += stride) {
+      const Work w = work_of<NT, STEP, BX>(a, grp, xt, yt, i, ge);
+      const ScaleBlock b = scale_block(a, w, blk, w.x0 + rank * 128, ks);
+      const int nch = chunks_of(w);
+      for (int q = 0; q < nch; ++q, ++ch) {
+        if ((ch & 1) != mine) continue;
+        const uint32_t cs = ch % kChunkSlots, use = ch / kChunkSlots;
+        ok = move_chunk<4>(b, q, ks, chunks + cs * kChunkBytes + blk * kWords * kWordBytes, [&] {
+          return use == 0 || warp_wait(&sempty[cs], (use - 1) & 1, abort_flag, a.status, 50);
+        });
+        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sfull[cs]);
+      }
+    }
+  } else if (warp < kEpi0) {
+    // -------------------------------------------------------- scale writers
+    const int q = warp & 3;
+    const uint32_t cols = tmem + (static_cast<uint32_t>(q * 32) << 16) + 2 * NT;
+    const uint32_t to = tc::cluster_addr(ready, 0);
+    uint32_t ch = 0, s = 0, slot = 0;
+    // the slot of stage g was last read by the MMAs of stage g - SLOTS
+    uint32_t old = 0, old_phase = 0;
+    bool ok = true, full_once = false;
+    for (uint32_t i = first; ok && i < n_work; i += stride) {
+      const Work w = work_of<NT, STEP, BX>(a, grp, xt, yt, i, ge);
+      const int nst = pair_stages(w);
+      for (int st = 0; st < nst; ++st) {
+        const int cw = st % SPC;
+        const uint32_t cs = ch % kChunkSlots;
+        if (cw == 0 && !warp_wait(&sfull[cs], (ch / kChunkSlots) & 1, abort_flag, a.status, 20)) {
+          ok = false;
+          break;
+        }
+        const uint8_t* src = chunks + cs * kChunkBytes + cw * 2 * WPS * kWordBytes + lane * 16;
+        uint32_t r[SF / 8][8];  // columns: [word 0: B, A, A][word 1: B, A, A]..., 4 columns each
+#pragma unroll
+        for (int j = 0; j < SF / 4; ++j) {
+          const int h = j / (1 + YB), b = j % (1 + YB);
+          const uint4 v = *reinterpret_cast<const uint4*>(src + (b * kWords + h) * kWordBytes);
+          r[j >> 1][(j & 1) * 4] = v.x;
+          r[j >> 1][(j & 1) * 4 + 1] = v.y;
+          r[j >> 1][(j & 1) * 4 + 2] = v.z;
+          r[j >> 1][(j & 1) * 4 + 3] = v.w;
+        }
+        if (full_once) {
+          if (!lead_wait(&empty[old], old_phase, abort_flag, a.status)) {
+            ok = false;
+            break;
+          }
+          if (++old == NS) {
+            old = 0;
+            old_phase ^= 1u;
+          }
+        }
+        tc::tc_fence_after();
+#pragma unroll
+        for (int j = 0; j < SF / 8; ++j) tc::tmem_st8(cols + slot * SF + 8 * j, r[j]);
+        tc::tmem_st_wait();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive_cluster(to + s * 8);
+        if (++s == NS) s = 0;
+        if (++slot == SLOTS) {
+          slot = 0;
+          full_once = true;
+        }
+        if (cw == SPC - 1 || st == nst - 1) {
+          if (lane == 0) tc::mbar_arrive(&sempty[cs]);
+          ++ch;
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------- epilogue
+    const int q = warp & 3;  // the lane quarter this warp may read
+    const int part = (warp - kEpi0) >> 2;
+    const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
+    uint32_t it = 0;
+    for (uint32_t i = first; i < n_work; i += stride, ++it) {
+      const Work w = work_of<NT, STEP, BX>(a, grp, xt, yt, i, ge);
+      const uint32_t b = it & 1;
+      if (!warp_wait(&dfull[b], (it >> 1) & 1, abort_flag, a.status, 100)) break;
+      tc::tc_fence_after();
+      const int64_t n = static_cast<int64_t>(w.x0) + rank * 128 + q * 32 + lane;
+      const uint32_t acc = tmem + b * NT + lane_base;
+      // the tile's columns, split over this quarter's two warps in steps of 32
+      const int all = (w.ny + 15) & ~15, half = (all / 2 + 31) & ~31;
+      const int c0 = part ? min(half, all) : 0, c1 = part ? all : min(half, all);
+      if (a.out_f32)
+        store_columns<true>(acc, a, w, n, c0, c1);
+      else
+        store_columns<false>(acc, a, w, n, c0, c1);
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive_cluster(tc::cluster_addr(&dempty[b], 0));
+    }
+  }
+
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    if (lane == 0) tc::mbar_drain(drain, 0, kWaitLimitNs / 8);
+    __syncwarp();
+  }
+  tc::cluster_sync();  // neither CTA touches the other's memory from here on
+  if (warp == 1) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc_pair(tmem, TMEM);
+  }
+}
+
+}  // namespace
+
+namespace mm {
+
+moe_status launch_pair(const Args& a, const uint8_t* xq, const uint8_t* yq, cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return MOE_ERR_CUDA;
+  }
+  const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
+  if (!bit || !(done.load() & bit)) {
+    if (cudaFuncSetAttribute(mxfp4_matmul_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kSmem) != cudaSuccess) {
+      cudaGetLastError();
+      return MOE_ERR_CUDA;
+    }
+    done.fetch_or(bit);
+  }
+  CUtensorMap mx, my;
+  if (!encode_codes(&mx, xq, a.K / 2, a.x_rows, a.mode == kGrouped ? a.E : 1, 128) ||
+      !encode_codes(&my, yq, a.K / 2, a.y_rows, 1, NT / 2))
+    return MOE_ERR_CUDA;
+  const int64_t xt = (a.x_rows + BX - 1) / BX, yt = (a.y_rows + NT - 1) / NT;
+  const int64_t most = xt * (a.mode == kDense ? yt : (a.mode == kGrouped ? yt + a.E : yt * a.E));
+  const int64_t pairs = sm_count() / 2;
+  const dim3 grid(static_cast<unsigned>(2 * (most < pairs ? most : pairs)));
+  return launch(mxfp4_matmul_pair_kernel, grid, dim3(kThreads), kSmem, stream, mx, my, a);
+}
+
+}  // namespace mm
+}  // namespace moe
