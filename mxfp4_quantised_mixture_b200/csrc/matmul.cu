@@ -80,11 +80,8 @@ __global__ void __launch_bounds__(threads(NT), ctas_per_sm(NT))
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* chunks = smem + NS * STAGE;
   constexpr int kEpi = epi_warps(NT), kEpi0 = 2 + kScaleWarps;
-  Groups grp;
-  grp.pfx = reinterpret_cast<int*>(chunks + kChunkSlots * kChunkBytes);
-  grp.lo = grp.pfx + kMaxGroups + 2;
-  grp.n = grp.lo + kMaxGroups + 2;
-  uint64_t* full = reinterpret_cast<uint64_t*>(grp.n + kMaxGroups + 2);  // [NS] stage copies landed
+  const Groups grp = group_table(chunks + kChunkSlots * kChunkBytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(grp.width + kMaxGroups + 2);  // [NS] stage copies landed
   uint64_t* empty = full + kMaxStages;     // [NS] stage MMAs complete
   uint64_t* sfull = empty + kMaxStages;    // [2] scale chunk written
   uint64_t* sempty = sfull + kChunkSlots;  // [2] scale chunk read
@@ -118,14 +115,12 @@ __global__ void __launch_bounds__(threads(NT), ctas_per_sm(NT))
     tc::tmem_alloc(tmem_holder, TMEM);
     tc::tmem_relinquish();
   }
-  if (warp == 2 && a.mode != kDense) fill_groups<NT>(a, grp);
+  if (warp == 2) fill_groups<NT, STEP>(a, grp);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  const uint32_t xt = static_cast<uint32_t>((a.x_rows + BX - 1) / BX);
-  const uint32_t yt = static_cast<uint32_t>((a.y_rows + NT - 1) / NT);
-  const uint32_t n_work = tiles(a, grp, xt, yt);
+  const uint32_t n_work = tiles(a, grp);
   const int ks = static_cast<int>(a.K / 32);
   int ge = 0;  // this role's cursor over the groups
 
@@ -134,7 +129,7 @@ __global__ void __launch_bounds__(threads(NT), ctas_per_sm(NT))
     uint32_t s = 0, phase = 0, issued = 0;
     bool ok = true;
     for (uint32_t i = blockIdx.x; ok && i < n_work; i += gridDim.x) {
-      const Work w = work_of<NT, STEP, BX>(a, grp, xt, yt, i, ge);
+      const Work w = work_of<NT, STEP, BX>(a, grp, i, ge);
       const int nst = stages_of(w);
       for (int st = 0; st < nst; ++st) {
         if (issued >= NS && !all_wait(&empty[s], phase ^ 1u, abort_flag, a.status)) {
@@ -167,7 +162,7 @@ __global__ void __launch_bounds__(threads(NT), ctas_per_sm(NT))
     uint32_t old = 0, old_phase = 0;  // ring slot of stage g - 2
     bool ok = true;
     for (uint32_t i = blockIdx.x; ok && i < n_work; i += gridDim.x, ++it) {
-      const Work w = work_of<NT, STEP, BX>(a, grp, xt, yt, i, ge);
+      const Work w = work_of<NT, STEP, BX>(a, grp, i, ge);
       const uint32_t idesc = tc::idesc_mxf4(BX, (w.ny + STEP - 1) & ~(STEP - 1));
       const uint32_t d = tmem + (it & 1) * ACC;
       // accumulator it & 1 was last used by tile it - 2
@@ -247,7 +242,7 @@ __global__ void __launch_bounds__(threads(NT), ctas_per_sm(NT))
     uint32_t ch = 0;
     bool ok = true;
     for (uint32_t i = blockIdx.x; ok && i < n_work; i += gridDim.x) {
-      const Work w = work_of<NT, STEP, BX>(a, grp, xt, yt, i, ge);
+      const Work w = work_of<NT, STEP, BX>(a, grp, i, ge);
       const ScaleBlock b = scale_block(a, w, blk, w.x0, ks);
       const int nch = chunks_of(w);
       for (int q = 0; q < nch; ++q, ++ch) {
@@ -270,7 +265,7 @@ __global__ void __launch_bounds__(threads(NT), ctas_per_sm(NT))
     const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
     uint32_t it = 0;
     for (uint32_t i = blockIdx.x; i < n_work; i += gridDim.x, ++it) {
-      const Work w = work_of<NT, STEP, BX>(a, grp, xt, yt, i, ge);
+      const Work w = work_of<NT, STEP, BX>(a, grp, i, ge);
       const uint32_t b = it & 1;
       if (!warp_wait(&dfull[b], (it >> 1) & 1, abort_flag, a.status, 100)) break;
       tc::tc_fence_after();
@@ -280,10 +275,7 @@ __global__ void __launch_bounds__(threads(NT), ctas_per_sm(NT))
       const int all = (w.ny + 15) & ~15;
       const int half = kEpi == 8 ? (all / 2 + 31) & ~31 : all;
       const int c0 = part ? min(half, all) : 0, c1 = part ? all : min(half, all);
-      if (a.out_f32)
-        store_columns<true>(acc, a, w, n, c0, c1);
-      else
-        store_columns<false>(acc, a, w, n, c0, c1);
+      store_columns(acc, a, w, n, c0, c1);
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&dempty[b]);
@@ -303,8 +295,9 @@ __global__ void __launch_bounds__(threads(NT), ctas_per_sm(NT))
 // ------------------------------------------------------------ host helpers
 
 template <int NT>
-moe_status launch_nt(const Args& a, const uint8_t* xq, const uint8_t* yq, int64_t max_work,
-                     cudaStream_t stream) {
+moe_status launch_nt(Args a, const uint8_t* xq, const uint8_t* yq, cudaStream_t stream) {
+  const int64_t max_work = plan_tiles(&a, BX, NT);
+  if (max_work > kMaxTiles) return MOE_ERR_SHAPE;
   static std::atomic<uint64_t> done{0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) {
@@ -334,13 +327,11 @@ moe_status launch_nt(const Args& a, const uint8_t* xq, const uint8_t* yq, int64_
 moe_status run(Args a, const uint8_t* xq, const uint8_t* yq, int64_t rows, cudaStream_t stream) {
   if (rows > 128 && a.x_rows > 128) return launch_pair(a, xq, yq, stream);
   const int NT = rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= 64 ? 64 : 128));
-  const int64_t xt = (a.x_rows + BX - 1) / BX, yt = (a.y_rows + NT - 1) / NT;
-  const int64_t max_work = xt * (a.mode == kDense ? yt : (a.mode == kGrouped ? yt + a.E : yt * a.E));
   switch (NT) {
-    case 16: return launch_nt<16>(a, xq, yq, max_work, stream);
-    case 32: return launch_nt<32>(a, xq, yq, max_work, stream);
-    case 64: return launch_nt<64>(a, xq, yq, max_work, stream);
-    default: return launch_nt<128>(a, xq, yq, max_work, stream);
+    case 16: return launch_nt<16>(a, xq, yq, stream);
+    case 32: return launch_nt<32>(a, xq, yq, stream);
+    case 64: return launch_nt<64>(a, xq, yq, stream);
+    default: return launch_nt<128>(a, xq, yq, stream);
   }
 }
 

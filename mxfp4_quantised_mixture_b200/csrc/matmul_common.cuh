@@ -20,13 +20,33 @@ constexpr int kWords = 2 * kStagesPerChunk;
 constexpr int kWordBytes = 512;     // one scale word of 128 rows, in tcgen05.cp's order
 constexpr int kChunkSlots = 2;
 constexpr int kMaxStages = 8;
-constexpr int kTableBytes = 3 * (kMaxGroups + 2) * 4;  // group table
+constexpr int kTableBytes = 4 * (kMaxGroups + 2) * 4;  // group table
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr int64_t kMaxTiles = (int64_t(1) << 31) - (1 << 16);  // tile numbers, and a grid past them
 
 enum Mode : int { kDense = 0, kGrouped = 1, kWgrad = 2 };
 
+// Division by a number known at launch, as a multiplication: floor(i / d) =
+// floor(i m / 2^(32 + s)) for every i < 2^31 with m = ceil(2^(32 + s) / d),
+// s = ceil(log2 d) - 1 (Granlund and Montgomery, PLDI 1994: m d - 2^(32 + s) < d
+// <= 2^(s + 1), so the error i (m d - 2^(32+s)) / (d 2^(32+s)) stays below 1 / d).
+struct FastDiv {
+  uint32_t d, m;
+  int s;
+};
+inline FastDiv fast_div(uint32_t d) {
+  FastDiv f{d, 0u, -1};
+  while ((uint64_t(1) << (f.s + 1)) < d) ++f.s;
+  if (d > 1) f.m = static_cast<uint32_t>(((uint64_t(1) << (32 + f.s)) + d - 1) / d);
+  return f;
+}
+__device__ __forceinline__ uint32_t operator/(uint32_t i, const FastDiv& f) {
+  return f.d == 1 ? i : __umulhi(i, f.m) >> f.s;
+}
+
 struct Args {
   int mode, E;
+  FastDiv xt, yt;          // tiles along B's rows, and along A's
   const int32_t* offsets;  // grouped, wgrad
   const uint8_t* xs;       // scales of B, [rows][ks]
   const uint8_t* ys;       // scales of A, [rows][ks]
@@ -52,8 +72,17 @@ struct Work {
 // Every group's first unit (tile of A rows, or 128 positions), first row and
 // rows, in shared memory.
 struct Groups {
-  int *pfx, *lo, *n;
+  int *pfx, *lo, *n, *width;  // width: rows of a tile
 };
+
+__device__ __forceinline__ Groups group_table(void* at) {
+  Groups g;
+  g.pfx = static_cast<int*>(at);
+  g.lo = g.pfx + kMaxGroups + 2;
+  g.n = g.lo + kMaxGroups + 2;
+  g.width = g.n + kMaxGroups + 2;
+  return g;
+}
 
 // two fp32 -> bf16x2, round to nearest even (lo in the low half)
 __device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
@@ -106,22 +135,22 @@ __device__ __forceinline__ int tile_width(int n) {
 // share a few tiles of A rows.  `e` is the caller's cursor over the groups:
 // its tiles' numbers only rise.
 template <int NT, int STEP, int BX>
-__device__ __forceinline__ Work work_of(const Args& a, const Groups& g, uint32_t xt, uint32_t yt,
-                                        uint32_t i, int& e) {
+__device__ __forceinline__ Work work_of(const Args& a, const Groups& g, uint32_t i, int& e) {
   Work w;
-  uint32_t u = i / xt;
-  w.x0 = static_cast<int>(i - u * xt) * BX;
+  uint32_t u = i / a.xt;
+  w.x0 = static_cast<int>(i - u * a.xt.d) * BX;
   w.k0 = 0;
   w.steps = static_cast<int>((a.K + 63) / 64);
-  int lo = 0, n = static_cast<int>(a.y_rows);
+  int lo = 0, n = static_cast<int>(a.y_rows), width = g.width[kMaxGroups];
   if (a.mode == kGrouped) {
     while (static_cast<int>(u) >= g.pfx[e + 1]) ++e;
     u -= g.pfx[e];
     lo = g.lo[e];
     n = g.n[e];
+    width = g.width[e];
   } else if (a.mode == kWgrad) {
-    e = static_cast<int>(u / yt);
-    u -= e * yt;
+    e = static_cast<int>(u / a.yt);
+    u -= e * a.yt.d;
     // never past the capacity, whatever the offsets hold
     const int64_t k0 = static_cast<int64_t>(g.pfx[e]) * kGroupAlign;
     const int64_t room = a.K - k0;
@@ -129,7 +158,6 @@ __device__ __forceinline__ Work work_of(const Args& a, const Groups& g, uint32_t
     w.k0 = len > 0 ? static_cast<int>(k0) : 0;
     w.steps = static_cast<int>((len + 63) / 64);
   }
-  const int width = tile_width<NT, STEP>(n);
   w.e = e;
   w.y0 = lo + static_cast<int>(u) * width;
   w.ny = min(width, lo + n - w.y0);
@@ -195,80 +223,113 @@ __device__ __forceinline__ void align_words(const Pieces& r, const uint8_t* p, i
   }
 }
 
-// 16 accumulator columns (output rows row0 + c, c < ny - c0) of this lane's
-// output column n, times alpha, into out.
-template <bool F32>
-__device__ __forceinline__ void store16(const uint32_t (&r)[16], float alpha, void* out, int64_t row,
-                                        int64_t ld, int64_t n, bool live, int ny) {
-  if (F32) {
-    float* p = static_cast<float*>(out) + row * ld + n;
+// 16 accumulator columns of this lane's output column, times alpha, to p, p +
+// ld, ... (elements).  ALL: every row exists (else the first ny do).
+template <bool F32, bool ALL>
+__device__ __forceinline__ void store16(const uint32_t (&r)[16], float alpha, void* p, uint32_t ld, int ny) {
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      if (live && k < ny) *p = alpha * __uint_as_float(r[k]);
-      p += ld;
-    }
-  } else if ((ld & 1) == 0) {
-    // neighbouring lanes swap halves of a column pair, so each stores two
-    // output columns of one row: half the stores
-    const int odd = threadIdx.x & 1;
-    uint16_t* p = static_cast<uint16_t*>(out) + (row + odd) * ld + (n - odd);
-#pragma unroll
-    for (int k = 0; k < 16; k += 2) {
-      const float v0 = alpha * __uint_as_float(r[k]), v1 = alpha * __uint_as_float(r[k + 1]);
-      const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? v0 : v1, 1);
-      const uint32_t packed = odd ? cvt_bf16x2(got, v1) : cvt_bf16x2(v0, got);
-      if (live && k + odd < ny) *reinterpret_cast<uint32_t*>(p) = packed;
-      p += 2 * ld;
-    }
-  } else {
-    uint16_t* p = static_cast<uint16_t*>(out) + row * ld + n;
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const float v = alpha * __uint_as_float(r[k]);
-      if (live && k < ny) *p = static_cast<uint16_t>(cvt_bf16x2(v, v));
-      p += ld;
+  for (int k = 0; k < 16; ++k) {
+    const float v = alpha * __uint_as_float(r[k]);
+    if (ALL || k < ny) {
+      const uint64_t at = static_cast<uint64_t>(k) * ld;
+      if (F32)
+        static_cast<float*>(p)[at] = v;
+      else
+        static_cast<uint16_t*>(p)[at] = static_cast<uint16_t>(cvt_bf16x2(v, 0.f));
     }
   }
 }
 
+// The same in bf16 for an even ld: neighbouring lanes swap halves of a column
+// pair, so each stores two output columns of every second row: half the stores.
+template <bool ALL>
+__device__ __forceinline__ void store16_pairs(const uint32_t (&r)[16], float alpha, void* p, uint32_t ld,
+                                              int ny) {
+  const int odd = threadIdx.x & 1;
+  uint16_t* q = static_cast<uint16_t*>(p) + (odd ? static_cast<int64_t>(ld) - 1 : 0);
+  uint32_t got[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) got[k] = __shfl_xor_sync(0xFFFFFFFFu, odd ? r[2 * k] : r[2 * k + 1], 1);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float lo = alpha * __uint_as_float(odd ? got[k] : r[2 * k]);
+    const float hi = alpha * __uint_as_float(odd ? r[2 * k + 1] : got[k]);
+    if (ALL || 2 * k + odd < ny)
+      *reinterpret_cast<uint32_t*>(q + static_cast<uint64_t>(2 * k) * ld) = cvt_bf16x2(lo, hi);
+  }
+}
+
 // Columns [c0, c1) of a tile's accumulator (a multiple of 16 of them, the last
-// ones possibly past its ny rows).
-template <bool F32>
+// ones possibly past its ny rows), to output column n.
 __device__ __forceinline__ void store_columns(uint32_t acc, const Args& a, const Work& w, int64_t n,
                                               int c0, int c1) {
   const bool live = n < a.x_rows;
+  const uint32_t ld = static_cast<uint32_t>(a.x_rows);
+  const bool pairs = !a.out_f32 && (ld & 1) == 0;
+  char* p = static_cast<char*>(a.out) + ((w.out_row + c0) * a.x_rows + n) * (a.out_f32 ? 4 : 2);
+  const int64_t step = static_cast<int64_t>(16) * ld * (a.out_f32 ? 4 : 2);
+  uint32_t r[2][16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) r[0][k] = r[1][k] = 0u;  // an empty sum, if nothing is loaded
+  const auto put = [&](const uint32_t (&v)[16], int ny) {
+    if (pairs) {  // lanes 2j, 2j + 1 exist together
+      if (!live) ny = 0;
+      if (__all_sync(0xFFFFFFFFu, ny >= 16))
+        store16_pairs<true>(v, a.alpha, p, ld, ny);
+      else
+        store16_pairs<false>(v, a.alpha, p, ld, ny);
+    } else if (live) {
+      if (a.out_f32) {
+        if (ny >= 16)
+          store16<true, true>(v, a.alpha, p, ld, ny);
+        else
+          store16<true, false>(v, a.alpha, p, ld, ny);
+      } else {
+        store16<false, false>(v, a.alpha, p, ld, ny);
+      }
+    }
+    p += step;
+  };
   for (int c = c0; c < c1; c += 32) {
-    uint32_t r[2][16];
     const bool two = c + 16 < c1;
     if (w.steps > 0) {
       tc::tmem_ld16(acc + c, r[0]);
       if (two) tc::tmem_ld16(acc + c + 16, r[1]);
       tc::tmem_ld_wait();
-    } else {
-#pragma unroll
-      for (int k = 0; k < 16; ++k) r[0][k] = r[1][k] = 0u;  // an empty sum
     }
-    store16<F32>(r[0], a.alpha, a.out, w.out_row + c, a.x_rows, n, live, w.ny - c);
-    if (two) store16<F32>(r[1], a.alpha, a.out, w.out_row + c + 16, a.x_rows, n, live, w.ny - c - 16);
+    put(r[0], w.ny - c);
+    if (two) put(r[1], w.ny - c - 16);
   }
 }
 
 // The group table, by one whole warp (NT rows of A to a tile).
-template <int NT>
+template <int NT, int STEP>
 __device__ __forceinline__ void fill_groups(const Args& a, const Groups& g) {
+  if ((threadIdx.x & 31) == 0) g.width[kMaxGroups] = tile_width<NT, STEP>(static_cast<int>(a.y_rows));
+  if (a.mode == kDense) return;
   group_prefix(a.E, g.pfx, [&](int e) {
     int64_t lo, hi;
     group_rows(a.offsets, e, a.S, lo, hi);
     const int n = static_cast<int>(hi - lo);
     g.lo[e] = static_cast<int>(lo);
     g.n[e] = n;
+    g.width[e] = tile_width<NT, STEP>(n);
     return a.mode == kGrouped ? (n + NT - 1) / NT : (n + kGroupAlign - 1) / kGroupAlign;
   });
 }
 
 // Number of tiles of BX rows of B by up to NT rows of A.
-__device__ __forceinline__ uint32_t tiles(const Args& a, const Groups& g, uint32_t xt, uint32_t yt) {
-  return xt * (a.mode == kDense ? yt : (a.mode == kGrouped ? g.pfx[a.E] : yt * a.E));
+__device__ __forceinline__ uint32_t tiles(const Args& a, const Groups& g) {
+  return a.xt.d * (a.mode == kDense ? a.yt.d : (a.mode == kGrouped ? g.pfx[a.E] : a.yt.d * a.E));
+}
+
+// Host side of the same: the two tile counts into the arguments, and an upper
+// bound of the number of tiles.
+inline int64_t plan_tiles(Args* a, int bx, int nt) {
+  const int64_t xt = (a->x_rows + bx - 1) / bx, yt = (a->y_rows + nt - 1) / nt;
+  a->xt = fast_div(static_cast<uint32_t>(xt));
+  a->yt = fast_div(static_cast<uint32_t>(yt));
+  return xt * (a->mode == kDense ? yt : (a->mode == kGrouped ? yt + a->E : yt * a->E));
 }
 
 // Stages and scale chunks of a tile.
@@ -351,7 +412,7 @@ inline bool encode_codes(CUtensorMap* map, const void* base, int64_t row, int64_
 }
 
 // The two-CTA kernel (csrc/matmul_pair.cu).
-moe_status launch_pair(const Args& a, const uint8_t* xq, const uint8_t* yq, cudaStream_t stream);
+moe_status launch_pair(Args a, const uint8_t* xq, const uint8_t* yq, cudaStream_t stream);
 
 }  // namespace mm
 }  // namespace moe

@@ -19,10 +19,14 @@
 //                of the A rows, by TMA into its own shared memory
 //   warp 1       tensor-memory owner; in the first CTA the MMA issuer, in the
 //                second it tells the issuer that a stage's codes have landed
-//   warps 2-7    scale loaders: one per 128-row block (B, A, A), in two groups
-//                that take every second chunk of 1024 k
-//   warps 8-11   scale writers, one per lane quarter: a stage's words from shared
-//                to tensor memory, and the issuer told
+//   warps 2, 3   scale loaders: cp.async of chunks of 1024 k (32 bytes of a
+//                row, as the three aligned 16-byte pieces that cover them), three
+//                chunks deep.  (Register loads two deep held the products back by
+//                a third: the loads' latency under this kernel's own traffic is
+//                several microseconds.)
+//   warps 4-11   scale writers, two groups of one per lane quarter: a stage's
+//                bytes shifted into words and put into tensor memory, and the
+//                issuer told
 //   warps 12-19  epilogue, two per lane quarter, from a double-buffered
 //                accumulator
 // The issuer's commits reach both CTAs' barriers.  Every wait is bounded (2 s);
@@ -43,24 +47,28 @@ using namespace mm;
 constexpr int NT = 192;    // rows of A per tile
 constexpr int STEP = 32;   // in steps of the pair's N
 constexpr int BX = 256;    // rows of B per tile
-constexpr int YB = 2;      // 128-row blocks of A's scales
 constexpr int X_BYTES = 128 * BKB, Y_BYTES = NT / 2 * BKB, WINDOW = X_BYTES + Y_BYTES;
 constexpr int WPS = 2;                     // windows of 256 k per stage
 constexpr int STAGE = WPS * WINDOW;
 constexpr int STEPS = WPS * kStepsPerStage;  // MMAs of 64 k per stage
 constexpr int SPC = kStagesPerChunk / WPS;   // stages per scale chunk
-constexpr int kLoaders = 2 * (1 + YB), kWriters = 4, kEpi = 8;
-constexpr int kWriter0 = 2 + kLoaders, kEpi0 = kWriter0 + kWriters;
+constexpr int kWriters = 4, kEpi = 8;  // warps (writers: per group)
+constexpr int kWriter0 = 4, kEpi0 = 12;
 constexpr int kThreads = 32 * (kEpi0 + kEpi);
-constexpr int kChunkBytes = (1 + YB) * kWords * kWordBytes;
-constexpr int SFW = 4 * (1 + YB);      // scale columns of one word (128 k)
+constexpr int kRowsAtOnce = 21;  // rows of scales the two loader warps take at once
+// a scale chunk in shared memory: of every row the three aligned 16-byte pieces
+// that cover its 32 bytes
+constexpr int kRowBytes = 48, kRows = 128 + NT;
+constexpr int kChunkBytes = kRows * kRowBytes;
+constexpr int kSlots = 3;
+constexpr int SFW = 4 + 8;             // scale columns of one word (128 k): B's rows, A's rows
 constexpr int SF = 2 * WPS * SFW;      // of a stage
 constexpr int TMEM = 512;
 constexpr int SLOTS = 2;               // stages of scales in tensor memory
 static_assert(2 * NT + SLOTS * SF <= TMEM, "two accumulators and the scale slots");
 constexpr int NS = 3;  // copy ring
-static_assert(SLOTS <= NS, "a slot's last stage is found by its ring barrier");
-constexpr int kSmem = 1024 + NS * STAGE + kChunkSlots * kChunkBytes + kTableBytes + 512;
+static_assert(SLOTS == 2 && SLOTS <= NS, "a slot's last stage is found by its ring barrier");
+constexpr int kSmem = 1024 + NS * STAGE + kSlots * kChunkBytes + kTableBytes + 512;
 static_assert(NS <= kMaxStages && kSmem <= 227 * 1024, "shared memory");
 
 __device__ __forceinline__ int pair_stages(const Work& w) { return (w.steps + STEPS - 1) / STEPS; }
@@ -82,16 +90,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* chunks = smem + NS * STAGE;
-  Groups grp;
-  grp.pfx = reinterpret_cast<int*>(chunks + kChunkSlots * kChunkBytes);
-  grp.lo = grp.pfx + kMaxGroups + 2;
-  grp.n = grp.lo + kMaxGroups + 2;
-  uint64_t* full = reinterpret_cast<uint64_t*>(grp.n + kMaxGroups + 2);  // [NS] own copies landed
+  const Groups grp = group_table(chunks + kSlots * kChunkBytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(grp.width + kMaxGroups + 2);  // [NS] own copies landed
   uint64_t* ready = full + kMaxStages;     // [NS] both CTAs' codes and scales (first CTA)
   uint64_t* empty = ready + kMaxStages;    // [NS] stage MMAs complete
-  uint64_t* sfull = empty + kMaxStages;    // [2] scale chunk in shared memory
-  uint64_t* sempty = sfull + kChunkSlots;  // [2] scale chunk read
-  uint64_t* dfull = sempty + kChunkSlots;  // [2] accumulator complete
+  uint64_t* sfull = empty + kMaxStages;    // [3] scale chunk in shared memory
+  uint64_t* sempty = sfull + kSlots;       // [3] scale chunk read
+  uint64_t* dfull = sempty + kSlots;  // [2] accumulator complete
   uint64_t* dempty = dfull + 2;            // [2] accumulator read by both CTAs (first CTA)
   uint64_t* drain = dempty + 2;            // every MMA issued has completed
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
@@ -105,9 +110,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tc::mbar_init(&ready[s], 2 * kWriters + 1);
       tc::mbar_init(&empty[s], 1);
     }
-    for (int s = 0; s < kChunkSlots; ++s) {
-      tc::mbar_init(&sfull[s], 1 + YB);
-      tc::mbar_init(&sempty[s], kWriters);
+    for (int s = 0; s < kSlots; ++s) {
+      tc::mbar_init(&sfull[s], 64);
+      tc::mbar_init(&sempty[s], 2 * kWriters);
     }
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(&dfull[b], 1);
@@ -123,15 +128,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc::tmem_alloc_pair(tmem_holder, TMEM);
     tc::tmem_relinquish_pair();
   }
-  if (warp == 2 && a.mode != kDense) fill_groups<NT>(a, grp);
+  if (warp == 2) fill_groups<NT, STEP>(a, grp);
   tc::tc_fence_before();
   __syncthreads();
   tc::cluster_sync();  // both CTAs' barriers exist before either is told anything
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  const uint32_t xt = static_cast<uint32_t>((a.x_rows + BX - 1) / BX);
-  const uint32_t yt = static_cast<uint32_t>((a.y_rows + NT - 1) / NT);
-  const uint32_t n_work = tiles(a, grp, xt, yt);
+  const uint32_t n_work = tiles(a, grp);
   const uint32_t first = blockIdx.x >> 1, stride = gridDim.x >> 1;
   const int ks = static_cast<int>(a.K / 32);
   int ge = 0;  // this role's cursor over the groups
@@ -141,7 +144,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t s = 0, phase = 0, issued = 0;
     bool ok = true;
     for (uint32_t i = first; ok && i < n_work; i += stride) {
-      const Work w = work_of<NT, STEP, BX>(a, grp, xt, yt, i, ge);
+      const Work w = work_of<NT, STEP, BX>(a, grp, i, ge);
       const int nst = pair_stages(w), half = ((w.ny + STEP - 1) & ~(STEP - 1)) / 2;
       for (int st = 0; st < nst; ++st) {
         if (issued >= NS && !all_wait(&empty[s], phase ^ 1u, abort_flag, a.status)) {
@@ -178,7 +181,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t it = 0, s = 0, phase = 0, slot = 0;
       bool ok = true, any = false;
       for (uint32_t i = first; ok && i < n_work; i += stride, ++it) {
-        const Work w = work_of<NT, STEP, BX>(a, grp, xt, yt, i, ge);
+        const Work w = work_of<NT, STEP, BX>(a, grp, i, ge);
         const uint32_t idesc = tc::idesc_mxf4(BX, (w.ny + STEP - 1) & ~(STEP - 1));
         const uint32_t d = tmem + (it & 1) * NT;
         // accumulator it & 1 was last used by tile it - 2
@@ -236,7 +239,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t s = 0, phase = 0;
       bool ok = true;
       for (uint32_t i = first; ok && i < n_work; i += stride) {
-        const int nst = pair_stages(work_of<NT, STEP, BX>(a, grp, xt, yt, i, ge));
+        const int nst = pair_stages(work_of<NT, STEP, BX>(a, grp, i, ge));
         for (int st = 0; ok && st < nst; ++st) {
           ok = all_wait(&full[s], phase, abort_flag, a.status);
           if (ok && lane == 0) tc::mbar_arrive_cluster(to + s * 8);
@@ -249,91 +252,133 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp < kWriter0) {
     // -------------------------------------------------------- scale loaders
-    const uint32_t mine = static_cast<uint32_t>(warp - 2) / (1 + YB);
-    const int blk = (warp - 2) % (1 + YB);
-    uint32_t ch = 0;
+    // Three threads to a row, one per piece; a piece's bytes past its row's end
+    // (or the array's) are not read and become 0, as their codes are.
+    const int lt = (warp - 2) * 32 + lane;
+    const int r0 = lt / 3, piece = lt % 3;  // the 64th thread has none
+    uint32_t slot = 0, phase = 0, ch = 0;
     bool ok = true;
     for (uint32_t i = first; ok && i < n_work; i += stride) {
-      const Work w = work_of<NT, STEP, BX>(a, grp, xt, yt, i, ge);
-      const ScaleBlock b = scale_block(a, w, blk, w.x0 + rank * 128, ks);
-      const int nch = chunks_of(w);
+      const Work w = work_of<NT, STEP, BX>(a, grp, i, ge);
+      const int nch = chunks_of(w), left = ks - w.k0 / 32;
+      const int64_t x0 = static_cast<int64_t>(w.x0) + rank * 128;
+      const int xr = static_cast<int>(min(a.x_rows - x0, static_cast<int64_t>(128)));
+      const uint8_t* px = a.xs + (x0 + (a.mode == kGrouped ? w.e * a.x_rows : 0) + r0) * ks + w.k0 / 32;
+      const uint8_t* py = a.ys + (static_cast<int64_t>(w.y0) + r0) * ks + w.k0 / 32;
       for (int q = 0; q < nch; ++q, ++ch) {
-        if ((ch & 1) != mine) continue;
-        const uint32_t cs = ch % kChunkSlots, use = ch / kChunkSlots;
-        ok = move_chunk<4>(b, q, ks, chunks + cs * kChunkBytes + blk * kWords * kWordBytes, [&] {
-          return use == 0 || warp_wait(&sempty[cs], (use - 1) & 1, abort_flag, a.status, 50);
-        });
-        if (!ok) break;
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sfull[cs]);
-      }
-    }
-  } else if (warp < kEpi0) {
-    // -------------------------------------------------------- scale writers
-    const int q = warp & 3;
-    const uint32_t cols = tmem + (static_cast<uint32_t>(q * 32) << 16) + 2 * NT;
-    const uint32_t to = tc::cluster_addr(ready, 0);
-    uint32_t ch = 0, s = 0, slot = 0;
-    // the slot of stage g was last read by the MMAs of stage g - SLOTS
-    uint32_t old = 0, old_phase = 0;
-    bool ok = true, full_once = false;
-    for (uint32_t i = first; ok && i < n_work; i += stride) {
-      const Work w = work_of<NT, STEP, BX>(a, grp, xt, yt, i, ge);
-      const int nst = pair_stages(w);
-      for (int st = 0; st < nst; ++st) {
-        const int cw = st % SPC;
-        const uint32_t cs = ch % kChunkSlots;
-        if (cw == 0 && !warp_wait(&sfull[cs], (ch / kChunkSlots) & 1, abort_flag, a.status, 20)) {
+        if (ch >= kSlots && !warp_wait(&sempty[slot], phase ^ 1u, abort_flag, a.status, 50)) {
           ok = false;
           break;
         }
-        const uint8_t* src = chunks + cs * kChunkBytes + cw * 2 * WPS * kWordBytes + lane * 16;
-        uint32_t r[SF / 8][8];  // columns: [word 0: B, A, A][word 1: B, A, A]..., 4 columns each
+        const int byte = q * kWords * 4, n = min(32, left - byte);
+        const uint32_t dst = tc::smem_u32(chunks + slot * kChunkBytes) + r0 * kRowBytes + piece * 16;
+        const auto move = [&](const uint8_t* p, int row, int rows, int block) {
+          const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u);
+          const int bytes = row < rows ? max(0, min(16, mis + n - 16 * piece)) : 0;
+          tc::cp_async16(dst + (block + row - r0) * kRowBytes, bytes ? p - mis + 16 * piece : a.xs, bytes);
+        };
+        if (r0 < kRowsAtOnce) {
 #pragma unroll
-        for (int j = 0; j < SF / 4; ++j) {
-          const int h = j / (1 + YB), b = j % (1 + YB);
-          const uint4 v = *reinterpret_cast<const uint4*>(src + (b * kWords + h) * kWordBytes);
-          r[j >> 1][(j & 1) * 4] = v.x;
-          r[j >> 1][(j & 1) * 4 + 1] = v.y;
-          r[j >> 1][(j & 1) * 4 + 2] = v.z;
-          r[j >> 1][(j & 1) * 4 + 3] = v.w;
+          for (int j = 0; j < 128; j += kRowsAtOnce)
+            if (r0 + j < 128) move(px + j * ks + byte, r0 + j, xr, 0);
+#pragma unroll
+          for (int j = 0; j < NT; j += kRowsAtOnce)
+            if (r0 + j < NT) move(py + j * ks + byte, r0 + j, w.ny, 128);
         }
-        if (full_once) {
-          if (!lead_wait(&empty[old], old_phase, abort_flag, a.status)) {
+        tc::cp_async_arrive(&sfull[slot]);
+        if (++slot == kSlots) {
+          slot = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    tc::cp_async_wait_all();
+  } else if (warp < kEpi0) {
+    // -------------------------------------------------------- scale writers
+    // Lane l holds rows l + 32 c of both sides, which are column c of lane l in
+    // every quarter of tensor memory.  The two groups of four warps take every
+    // second stage each, and with it one of the two slots of scale columns.
+    const int q = warp & 3;
+    const uint32_t mine = static_cast<uint32_t>(warp - kWriter0) >> 2;
+    const uint32_t cols = tmem + (static_cast<uint32_t>(q * 32) << 16) + 2 * NT + mine * SF;
+    const uint32_t to = tc::cluster_addr(ready, 0);
+    uint32_t g = 0, s = 0, cs = 0, cphase = 0;
+    // the slot of stage g was last read by the MMAs of stage g - 2
+    uint32_t old = mine, old_phase = 0;
+    bool ok = true;
+    for (uint32_t i = first; ok && i < n_work; i += stride) {
+      const Work w = work_of<NT, STEP, BX>(a, grp, i, ge);
+      const int nst = pair_stages(w);
+      const int64_t x0 = static_cast<int64_t>(w.x0) + rank * 128;
+      // a row's misalignment: chunks are 32 bytes apart and a lane's rows 32 rows,
+      // so every chunk and every row of this lane has the same
+      const uint32_t mx = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
+          a.xs + (x0 + (a.mode == kGrouped ? w.e * a.x_rows : 0) + lane) * ks + w.k0 / 32)) & 15u;
+      const uint32_t my = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
+          a.ys + (static_cast<int64_t>(w.y0) + lane) * ks + w.k0 / 32)) & 15u;
+      for (int st = 0; st < nst; ++st, ++g) {
+        const int cw = st % SPC;
+        if ((g & 1) == mine) {
+          if (!warp_wait(&sfull[cs], cphase, abort_flag, a.status, 20)) {
             ok = false;
             break;
           }
-          if (++old == NS) {
-            old = 0;
-            old_phase ^= 1u;
-          }
-        }
-        tc::tc_fence_after();
+          const uint8_t* src = chunks + cs * kChunkBytes + lane * kRowBytes + cw * 16;
+          uint32_t r[SF];  // columns: [word 0: B 4, A 6, none 2][word 1: ...]...
 #pragma unroll
-        for (int j = 0; j < SF / 8; ++j) tc::tmem_st8(cols + slot * SF + 8 * j, r[j]);
-        tc::tmem_st_wait();
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive_cluster(to + s * 8);
-        if (++s == NS) s = 0;
-        if (++slot == SLOTS) {
-          slot = 0;
-          full_once = true;
+          for (int j = 0; j < kRows / 32; ++j) {
+            const uint32_t mis = j < 4 ? mx : my;
+            const uint4 lo = *reinterpret_cast<const uint4*>(src + 32 * j * kRowBytes);
+            const uint4 hi = *reinterpret_cast<const uint4*>(src + 32 * j * kRowBytes + 16);
+            uint32_t x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+            for (int k = 0; k < 7; ++k) x[k] = mis & 4u ? x[k + 1] : x[k];
+#pragma unroll
+            for (int k = 0; k < 5; ++k) x[k] = mis & 8u ? x[k + 2] : x[k];
+#pragma unroll
+            for (int k = 0; k < 2 * WPS; ++k) r[k * SFW + j] = __funnelshift_r(x[k], x[k + 1], (mis & 3u) * 8);
+          }
+#pragma unroll
+          for (int k = 0; k < 2 * WPS; ++k)
+#pragma unroll
+            for (int j = kRows / 32; j < SFW; ++j) r[k * SFW + j] = 0u;
+          if (g >= 2) {
+            if (!lead_wait(&empty[old], old_phase, abort_flag, a.status)) {
+              ok = false;
+              break;
+            }
+            if ((old += 2) >= NS) {
+              old -= NS;
+              old_phase ^= 1u;
+            }
+          }
+          tc::tc_fence_after();
+#pragma unroll
+          for (int j = 0; j < SF / 16; ++j)
+            tc::tmem_st16(cols + 16 * j, *reinterpret_cast<const uint32_t(*)[16]>(r + 16 * j));
+          tc::tmem_st_wait();
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive_cluster(to + s * 8);
         }
+        if (++s == NS) s = 0;
+        // both groups let a chunk go, whichever of its stages were theirs
         if (cw == SPC - 1 || st == nst - 1) {
           if (lane == 0) tc::mbar_arrive(&sempty[cs]);
-          ++ch;
+          if (++cs == kSlots) {
+            cs = 0;
+            cphase ^= 1u;
+          }
         }
       }
     }
   } else {
     // ------------------------------------------------------------- epilogue
     const int q = warp & 3;  // the lane quarter this warp may read
-    const int part = (warp - kEpi0) >> 2;
     const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
     uint32_t it = 0;
     for (uint32_t i = first; i < n_work; i += stride, ++it) {
-      const Work w = work_of<NT, STEP, BX>(a, grp, xt, yt, i, ge);
+      const Work w = work_of<NT, STEP, BX>(a, grp, i, ge);
       const uint32_t b = it & 1;
       if (!warp_wait(&dfull[b], (it >> 1) & 1, abort_flag, a.status, 100)) break;
       tc::tc_fence_after();
@@ -341,11 +386,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t acc = tmem + b * NT + lane_base;
       // the tile's columns, split over this quarter's two warps in steps of 32
       const int all = (w.ny + 15) & ~15, half = (all / 2 + 31) & ~31;
+      const int part = (warp - kEpi0) >> 2;
       const int c0 = part ? min(half, all) : 0, c1 = part ? all : min(half, all);
-      if (a.out_f32)
-        store_columns<true>(acc, a, w, n, c0, c1);
-      else
-        store_columns<false>(acc, a, w, n, c0, c1);
+      store_columns(acc, a, w, n, c0, c1);
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive_cluster(tc::cluster_addr(&dempty[b], 0));
@@ -369,7 +412,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 namespace mm {
 
-moe_status launch_pair(const Args& a, const uint8_t* xq, const uint8_t* yq, cudaStream_t stream) {
+moe_status launch_pair(Args a, const uint8_t* xq, const uint8_t* yq, cudaStream_t stream) {
+  const int64_t most = plan_tiles(&a, BX, NT);
+  if (most > kMaxTiles) return MOE_ERR_SHAPE;
   static std::atomic<uint64_t> done{0};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) {
@@ -389,8 +434,6 @@ moe_status launch_pair(const Args& a, const uint8_t* xq, const uint8_t* yq, cuda
   if (!encode_codes(&mx, xq, a.K / 2, a.x_rows, a.mode == kGrouped ? a.E : 1, 128) ||
       !encode_codes(&my, yq, a.K / 2, a.y_rows, 1, NT / 2))
     return MOE_ERR_CUDA;
-  const int64_t xt = (a.x_rows + BX - 1) / BX, yt = (a.y_rows + NT - 1) / NT;
-  const int64_t most = xt * (a.mode == kDense ? yt : (a.mode == kGrouped ? yt + a.E : yt * a.E));
   const int64_t pairs = sm_count() / 2;
   const dim3 grid(static_cast<unsigned>(2 * (most < pairs ? most : pairs)));
   return launch(mxfp4_matmul_pair_kernel, grid, dim3(kThreads), kSmem, stream, mx, my, a);
