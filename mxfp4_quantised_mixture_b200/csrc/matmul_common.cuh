@@ -240,22 +240,21 @@ __device__ __forceinline__ void store16(const uint32_t (&r)[16], float alpha, vo
   }
 }
 
-// The same in bf16 for an even ld: neighbouring lanes swap halves of a column
-// pair, so each stores two output columns of every second row: half the stores.
+// The same in bf16 for an even ld: two rows are packed, then neighbouring lanes
+// swap halves, so each lane stores two output columns of every second row: half
+// the stores.  p is the lane's own row and column (odd lanes: the next row, the
+// column before).
 template <bool ALL>
-__device__ __forceinline__ void store16_pairs(const uint32_t (&r)[16], float alpha, void* p, uint32_t ld,
+__device__ __forceinline__ void store16_pairs(const uint32_t (&r)[16], float alpha, char* p, uint32_t ld2,
                                               int ny) {
   const int odd = threadIdx.x & 1;
-  uint16_t* q = static_cast<uint16_t*>(p) + (odd ? static_cast<int64_t>(ld) - 1 : 0);
-  uint32_t got[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) got[k] = __shfl_xor_sync(0xFFFFFFFFu, odd ? r[2 * k] : r[2 * k + 1], 1);
+  const uint32_t pick = odd ? 0x3276u : 0x5410u;  // the other's high half and mine, or my low half and its
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const float lo = alpha * __uint_as_float(odd ? got[k] : r[2 * k]);
-    const float hi = alpha * __uint_as_float(odd ? r[2 * k + 1] : got[k]);
+    const uint32_t own = cvt_bf16x2(alpha * __uint_as_float(r[2 * k]), alpha * __uint_as_float(r[2 * k + 1]));
+    const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, own, 1);
     if (ALL || 2 * k + odd < ny)
-      *reinterpret_cast<uint32_t*>(q + static_cast<uint64_t>(2 * k) * ld) = cvt_bf16x2(lo, hi);
+      *reinterpret_cast<uint32_t*>(p + static_cast<uint64_t>(k) * 2 * ld2) = __byte_perm(own, got, pick);
   }
 }
 
@@ -266,8 +265,10 @@ __device__ __forceinline__ void store_columns(uint32_t acc, const Args& a, const
   const bool live = n < a.x_rows;
   const uint32_t ld = static_cast<uint32_t>(a.x_rows);
   const bool pairs = !a.out_f32 && (ld & 1) == 0;
-  char* p = static_cast<char*>(a.out) + ((w.out_row + c0) * a.x_rows + n) * (a.out_f32 ? 4 : 2);
-  const int64_t step = static_cast<int64_t>(16) * ld * (a.out_f32 ? 4 : 2);
+  const int size = a.out_f32 ? 4 : 2;
+  char* p = static_cast<char*>(a.out) + ((w.out_row + c0) * a.x_rows + n) * size;
+  if (pairs && (threadIdx.x & 1)) p += static_cast<int64_t>(ld) * 2 - 2;
+  const int64_t step = static_cast<int64_t>(16) * ld * size;
   uint32_t r[2][16];
 #pragma unroll
   for (int k = 0; k < 16; ++k) r[0][k] = r[1][k] = 0u;  // an empty sum, if nothing is loaded
@@ -275,9 +276,9 @@ __device__ __forceinline__ void store_columns(uint32_t acc, const Args& a, const
     if (pairs) {  // lanes 2j, 2j + 1 exist together
       if (!live) ny = 0;
       if (__all_sync(0xFFFFFFFFu, ny >= 16))
-        store16_pairs<true>(v, a.alpha, p, ld, ny);
+        store16_pairs<true>(v, a.alpha, p, 2 * ld, ny);
       else
-        store16_pairs<false>(v, a.alpha, p, ld, ny);
+        store16_pairs<false>(v, a.alpha, p, 2 * ld, ny);
     } else if (live) {
       if (a.out_f32) {
         if (ny >= 16)
