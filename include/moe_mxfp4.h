@@ -343,7 +343,7 @@ MOE_API int64_t mxfp4_transposed_width(int64_t rows, int32_t E);
  * positions from `rows` to P zero.
  *   w_bf16   in   [batch][rows][cols] bf16
  *   batch    in   >= 0;  rows in >= 0 (either 0: a no-op), rows <= 2^31
- *   cols     in   multiple of 8, >= 8;  batch*rows*cols <= 2^40
+ *   cols     in   multiple of 8 in [8, 2^31];  batch*rows*cols <= 2^40
  *   q_packed out  [batch][cols][P/2], P = mxfp4_transposed_width(rows, 0)
  *   scales   out  [batch][cols][P/32]
  *   d_status out  nullable; MOE_ERR_NONFINITE if a block holds NaN or Inf

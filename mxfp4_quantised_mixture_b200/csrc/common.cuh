@@ -33,6 +33,26 @@ __device__ __forceinline__ void record_status(int32_t* status, int32_t code) {
   if (status) atomicCAS(status, static_cast<int32_t>(MOE_OK), code);
 }
 
+// ------------------------------------------------- division by multiplication
+
+// Division by a number known at launch, as a multiplication: floor(i / d) =
+// floor(i m / 2^(32 + s)) for every i < 2^31 with m = ceil(2^(32 + s) / d),
+// s = ceil(log2 d) - 1 (Granlund and Montgomery, PLDI 1994: m d - 2^(32 + s) < d
+// <= 2^(s + 1), so the error i (m d - 2^(32+s)) / (d 2^(32+s)) stays below 1 / d).
+struct FastDiv {
+  uint32_t d, m;
+  int s;
+};
+inline FastDiv fast_div(uint32_t d) {
+  FastDiv f{d, 0u, -1};
+  while ((uint64_t(1) << (f.s + 1)) < d) ++f.s;
+  if (d > 1) f.m = static_cast<uint32_t>(((uint64_t(1) << (32 + f.s)) + d - 1) / d);
+  return f;
+}
+__device__ __forceinline__ uint32_t operator/(uint32_t i, const FastDiv& f) {
+  return f.d == 1 ? i : __umulhi(i, f.m) >> f.s;
+}
+
 // ------------------------------------------------------------ host helpers
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

@@ -32,24 +32,22 @@ template <int K, bool ROUTER>
 __global__ void __launch_bounds__(kThreads)
     permute_backward_kernel(const uint4* __restrict__ dx_perm, const int32_t* __restrict__ slot_pos,
                             const int32_t* __restrict__ idx, const float* __restrict__ dscore,
-                            const uint4* __restrict__ w_router, int E, int64_t T, int64_t S,
-                            int vec_per_row, uint4* __restrict__ dx) {
-  const int64_t n = T * vec_per_row;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < n;
-       i += static_cast<int64_t>(gridDim.x) * kThreads) {
-    const int64_t t = i / vec_per_row;
-    const int v = static_cast<int>(i - t * vec_per_row);
+                            const uint4* __restrict__ w_router, int E, uint32_t n, int S,
+                            FastDiv vec_per_row, uint4* __restrict__ dx) {
+  for (uint32_t i = blockIdx.x * kThreads + threadIdx.x; i < n; i += gridDim.x * kThreads) {
+    const uint32_t t = i / vec_per_row;
+    const int v = static_cast<int>(i - t * vec_per_row.d);
     uint4 r[K], wr[K];
     float ds[K];
 #pragma unroll
     for (int j = 0; j < K; ++j) {
       const int32_t p = __ldg(slot_pos + t * K + j);
-      r[j] = p >= 0 && p < S ? __ldg(dx_perm + static_cast<int64_t>(p) * vec_per_row + v)
+      r[j] = p >= 0 && p < S ? __ldg(dx_perm + static_cast<int64_t>(p) * vec_per_row.d + v)
                              : make_uint4(0u, 0u, 0u, 0u);
       if (ROUTER) {
         const int e = __ldg(idx + t * K + j);
         const bool in = static_cast<unsigned>(e) < static_cast<unsigned>(E);
-        wr[j] = in ? __ldg(w_router + static_cast<int64_t>(e) * vec_per_row + v)
+        wr[j] = in ? __ldg(w_router + static_cast<int64_t>(e) * vec_per_row.d + v)
                    : make_uint4(0u, 0u, 0u, 0u);
         ds[j] = in ? __ldg(dscore + t * K + j) : 0.f;
       }
@@ -80,14 +78,17 @@ moe_status launch_k(cudaStream_t stream, const uint16_t* dx_perm, const int32_t*
   const int64_t want = (static_cast<int64_t>(sh.T) * vec + kThreads - 1) / kThreads;
   const int64_t cap = static_cast<int64_t>(sm_count()) * 16;
   const dim3 grid(static_cast<unsigned>(want < cap ? want : cap));
-  const int64_t T = sh.T, S = T * sh.k;
+  // T D / 8 <= 2^31: every index fits the division by multiplication
+  const uint32_t n = static_cast<uint32_t>(static_cast<int64_t>(sh.T) * vec);
+  const int S = sh.T * sh.k;
+  const FastDiv fd = fast_div(static_cast<uint32_t>(vec));
   const uint4* in = reinterpret_cast<const uint4*>(dx_perm);
   const uint4* wr = reinterpret_cast<const uint4*>(w_router);
   uint4* out = reinterpret_cast<uint4*>(dx);
   return w_router ? launch(permute_backward_kernel<K, true>, grid, dim3(kThreads), 0, stream, in,
-                           slot_pos, idx, dscore, wr, sh.E, T, S, vec, out)
+                           slot_pos, idx, dscore, wr, sh.E, n, S, fd, out)
                   : launch(permute_backward_kernel<K, false>, grid, dim3(kThreads), 0, stream, in,
-                           slot_pos, idx, dscore, wr, sh.E, T, S, vec, out);
+                           slot_pos, idx, dscore, wr, sh.E, n, S, fd, out);
 }
 
 }  // namespace

@@ -32,7 +32,8 @@ constexpr int kRows = 128, kCols = 128;
 template <bool GROUPED>
 __global__ void __launch_bounds__(kThreads)
     quantize_transposed_kernel(const uint32_t* __restrict__ w, int64_t rows, int64_t cols,
-                               int64_t batch, const int32_t* __restrict__ offsets, int E, int64_t P,
+                               uint32_t batch, const int32_t* __restrict__ offsets, int E, int64_t P,
+                               FastDiv col_tiles, FastDiv row_tiles,
                                uint8_t* __restrict__ q, uint8_t* __restrict__ s,
                                int32_t* __restrict__ status) {
   __shared__ uint4 codes[kCols * 4];
@@ -41,8 +42,7 @@ __global__ void __launch_bounds__(kThreads)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rb = warp & 3;                       // 32-row block of the tile
   const int lc = (warp >> 2) * 64 + lane * 2;    // first of this lane's two columns
-  const int64_t col_tiles = (cols + kCols - 1) / kCols;
-  int64_t row_tiles = (P + kRows - 1) / kRows;
+  uint32_t n_tiles = batch * row_tiles.d * col_tiles.d;
   if (GROUPED) {
     if (warp == 0)
       group_prefix(E, pfx, [&](int e) {
@@ -51,28 +51,33 @@ __global__ void __launch_bounds__(kThreads)
         return (hi - lo + kGroupAlign - 1) / kGroupAlign;
       });
     __syncthreads();
-    row_tiles = min(row_tiles, pfx[E]);
+    // no tile behind the last group's, nor past the output whatever the offsets hold
+    n_tiles = min(static_cast<int64_t>(row_tiles.d), pfx[E]) * col_tiles.d;
   }
-  const int64_t n_tiles = batch * row_tiles * col_tiles;
-  for (int64_t i = blockIdx.x; i < n_tiles; i += gridDim.x) {
-    const int64_t ct = i % col_tiles;
-    const int64_t rt = i / col_tiles % row_tiles;
-    const int64_t b = i / col_tiles / row_tiles;
-    int64_t r0 = rt * kRows, r_end = rows;  // source rows of the tile: [r0, r_end)
+  const uint32_t pitch = static_cast<uint32_t>(cols / 2);  // words of a row
+  for (uint32_t i = blockIdx.x; i < n_tiles; i += gridDim.x) {
+    const uint32_t it = i / col_tiles, ct = i - it * col_tiles.d;
+    const uint32_t b = GROUPED ? 0u : it / row_tiles, rt = it - b * row_tiles.d;
+    int64_t r0 = static_cast<int64_t>(rt) * kRows, r_end = rows;  // source rows of the tile: [r0, r_end)
     if (GROUPED) {
       const int e = group_of(pfx, E, rt);
       int64_t lo;
       group_rows(offsets, e, rows, lo, r_end);
       r0 = lo + (rt - pfx[e]) * kRows;
     }
-    const int64_t c0 = ct * kCols;
+    const int64_t c0 = static_cast<int64_t>(ct) * kCols;
     const bool col_ok = c0 + lc < cols;  // cols is even
     const int64_t rs = r0 + rb * 32;
-    const uint32_t* src = w + (b * rows + rs) * (cols / 2) + (c0 + lc) / 2;
+    const int n = col_ok ? static_cast<int>(min(max(r_end - rs, int64_t(0)), int64_t(32))) : 0;
+    const uint32_t* src = w + (b * rows + rs) * static_cast<int64_t>(pitch) + (c0 + lc) / 2;
     uint32_t v[32];
+    if (n == 32) {
 #pragma unroll
-    for (int k = 0; k < 32; ++k)
-      v[k] = col_ok && rs + k < r_end ? __ldg(src + k * (cols / 2)) : 0u;
+      for (int k = 0; k < 32; ++k) v[k] = __ldg(src + static_cast<uint64_t>(k) * pitch);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) v[k] = k < n ? __ldg(src + static_cast<uint64_t>(k) * pitch) : 0u;
+    }
     uint32_t m2 = 0;
 #pragma unroll
     for (int k = 0; k < 32; ++k) m2 = __vmaxu2(m2, v[k] & 0x7FFF7FFFu);
@@ -100,9 +105,10 @@ __global__ void __launch_bounds__(kThreads)
       if (m >= 0x7F80u) record_status(status, MOE_ERR_NONFINITE);
     }
     __syncthreads();
-    const int64_t p0 = rt * kRows;  // first output position
-    for (int j = threadIdx.x; j < kCols * 4; j += kThreads) {
-      const int col = j >> 2, blk = j & 3, line = col >> 1;
+    const int64_t p0 = static_cast<int64_t>(rt) * kRows;  // first output position
+#pragma unroll
+    for (int k = 0; k < kCols * 4 / kThreads; ++k) {
+      const int j = threadIdx.x + k * kThreads, col = j >> 2, blk = j & 3, line = col >> 1;
       if (c0 + col < cols && p0 + blk * 32 < P)
         *reinterpret_cast<uint4*>(q + (b * cols + c0 + col) * (P / 2) + p0 / 2 + blk * 16) =
             codes[line * 8 + (((col & 1) * 4 + blk) ^ (line & 7))];
@@ -130,15 +136,23 @@ moe_status check(const uint16_t* w, int64_t n, const uint8_t* q, const uint8_t* 
   return MOE_OK;
 }
 
-int grid_for(int64_t tiles) {
+template <bool GROUPED>
+moe_status launch_tiles(const uint16_t* w, int64_t batch, int64_t rows, int64_t cols, const int32_t* offsets,
+                        int32_t E, int64_t P, uint8_t* q, uint8_t* s, int32_t* d_status, moe_stream stream) {
+  const int64_t ct = (cols + kCols - 1) / kCols, rt = (P + kRows - 1) / kRows;
   const int64_t cap = static_cast<int64_t>(sm_count()) * 8;
-  return static_cast<int>(tiles < cap ? tiles : cap);
+  if (batch * rt >= (int64_t(1) << 31) / ct - cap) return MOE_ERR_SHAPE;
+  const int64_t tiles = batch * rt * ct;
+  return launch(quantize_transposed_kernel<GROUPED>, dim3(static_cast<unsigned>(tiles < cap ? tiles : cap)),
+                dim3(kThreads), 0, static_cast<cudaStream_t>(stream), reinterpret_cast<const uint32_t*>(w),
+                rows, cols, static_cast<uint32_t>(batch), offsets, E, P, fast_div(static_cast<uint32_t>(ct)),
+                fast_div(static_cast<uint32_t>(rt)), q, s, d_status);
 }
 
 bool sizes_ok(int64_t batch, int64_t rows, int64_t cols) {
   if (batch < 0 || rows < 0 || cols < 8 || cols % 8) return false;
   const int64_t lim = int64_t(1) << 40;
-  if (rows > (int64_t(1) << 31) || cols > lim || batch > lim) return false;
+  if (rows > (int64_t(1) << 31) || cols > (int64_t(1) << 31) || batch > lim) return false;
   if (rows > 0 && (cols > lim / rows || (batch > 0 && batch > lim / (rows * cols)))) return false;
   return true;
 }
@@ -164,11 +178,8 @@ moe_status mxfp4_quantize_transposed(const uint16_t* w_bf16, int64_t batch, int6
   moe_status st = check(w_bf16, batch * rows, q_packed, scales, d_status);
   if (st != MOE_OK) return st;
   if ((st = check_device()) != MOE_OK) return st;
-  const int64_t P = mxfp4_transposed_width(rows, 0);
-  const int64_t tiles = batch * ((P + kRows - 1) / kRows) * ((cols + kCols - 1) / kCols);
-  return launch(quantize_transposed_kernel<false>, dim3(grid_for(tiles)), dim3(kThreads), 0,
-                static_cast<cudaStream_t>(stream), reinterpret_cast<const uint32_t*>(w_bf16), rows,
-                cols, batch, static_cast<const int32_t*>(nullptr), 0, P, q_packed, scales, d_status);
+  return launch_tiles<false>(w_bf16, batch, rows, cols, nullptr, 0, mxfp4_transposed_width(rows, 0),
+                             q_packed, scales, d_status, stream);
 }
 
 moe_status mxfp4_quantize_transposed_grouped(const uint16_t* w_bf16, int64_t rows, int64_t cols,
@@ -183,10 +194,7 @@ moe_status mxfp4_quantize_transposed_grouped(const uint16_t* w_bf16, int64_t row
   moe_status st = check(w_bf16, rows, q_packed, scales, d_status);
   if (st != MOE_OK) return st;
   if ((st = check_device()) != MOE_OK) return st;
-  const int64_t tiles = (P / kRows) * ((cols + kCols - 1) / kCols);
-  return launch(quantize_transposed_kernel<true>, dim3(grid_for(tiles)), dim3(kThreads), 0,
-                static_cast<cudaStream_t>(stream), reinterpret_cast<const uint32_t*>(w_bf16), rows,
-                cols, int64_t(1), offsets, E, P, q_packed, scales, d_status);
+  return launch_tiles<true>(w_bf16, 1, rows, cols, offsets, E, P, q_packed, scales, d_status, stream);
 }
 
 }  // extern "C"
