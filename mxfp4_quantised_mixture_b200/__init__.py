@@ -137,7 +137,8 @@ def _s(stream) -> int | None:
     if stream is None:
         import torch
 
-        return torch.cuda.current_stream().cuda_stream
+        # the current device's current stream, without building a Stream object
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -195,18 +196,20 @@ def _sizes(fn: str, ok: bool) -> None:
 def _out_type(fn: str, out) -> int:
     import torch
 
-    if out.dtype == torch.bfloat16:
+    if out.dtype is torch.bfloat16:
         return MOE_OUT_BF16
-    if out.dtype == torch.float32:
+    if out.dtype is torch.float32:
         return MOE_OUT_FP32
     raise ValueError(f"{fn}: the output is bfloat16 or float32, not {out.dtype}")
 
 
-def _mx_ok(q, s, K: int) -> bool:
+def _mx_ok(q, s, lead: tuple, K: int) -> bool:
+    """Codes and scales of an MXFP4 tensor [*lead, K]."""
     import torch
 
-    return (q.dtype == torch.uint8 and s.dtype == torch.uint8 and q.shape[:-1] == s.shape[:-1]
-            and 2 * q.shape[-1] == K and 32 * s.shape[-1] == K)
+    u8 = torch.uint8
+    return (K % 32 == 0 and q.dtype is u8 and s.dtype is u8 and q.shape == lead + (K // 2,)
+            and s.shape == lead + (K // 32,))
 
 
 def mxfp4_transposed_width(rows: int, E: int = 0) -> int:
@@ -222,8 +225,8 @@ def mxfp4_quantize_transposed(w_bf16, q_packed, scales, d_status=None, stream=No
     fn = "mxfp4_quantize_transposed"
     R, C = w_bf16.shape[-2:]
     P = mxfp4_transposed_width(R)
-    _sizes(fn, w_bf16.element_size() == 2 and _mx_ok(q_packed, scales, P)
-           and q_packed.shape[:-1] == w_bf16.shape[:-2] + (C,))
+    _sizes(fn, w_bf16.element_size() == 2
+           and _mx_ok(q_packed, scales, tuple(w_bf16.shape[:-2]) + (C,), P))
     batch = w_bf16.numel() // (R * C) if R * C else 0
     _check(fn, lib.mxfp4_quantize_transposed(_p(w_bf16), batch, R, C, _p(q_packed), _p(scales),
                                              _p(d_status), _s(stream)))
@@ -238,7 +241,7 @@ def mxfp4_quantize_transposed_grouped(w_bf16, offsets, q_packed, scales, d_statu
     E = offsets.numel() - 1
     P = mxfp4_transposed_width(S, E)
     _sizes(fn, w_bf16.element_size() == 2 and offsets.element_size() == 4
-           and _mx_ok(q_packed, scales, P) and tuple(q_packed.shape[:-1]) == (C,))
+           and _mx_ok(q_packed, scales, (C,), P))
     _check(fn, lib.mxfp4_quantize_transposed_grouped(_p(w_bf16), S, C, _p(offsets), E,
                                                      _p(q_packed), _p(scales), _p(d_status),
                                                      _s(stream)))
@@ -248,8 +251,7 @@ def mxfp4_matmul(a_q, a_s, b_q, b_s, out, alpha: float = 1.0, d_status=None, str
     """out [M, N] (bf16 or fp32) = alpha * A B^T of MXFP4 A [M, K] and B [N, K]."""
     fn = "mxfp4_matmul"
     (M, N), K = out.shape, 2 * a_q.shape[-1]
-    _sizes(fn, _mx_ok(a_q, a_s, K) and _mx_ok(b_q, b_s, K) and tuple(a_q.shape[:-1]) == (M,)
-           and tuple(b_q.shape[:-1]) == (N,))
+    _sizes(fn, _mx_ok(a_q, a_s, (M,), K) and _mx_ok(b_q, b_s, (N,), K))
     _check(fn, lib.mxfp4_matmul(_p(a_q), _p(a_s), _p(b_q), _p(b_s), M, N, K, float(alpha), _p(out),
                                 _out_type(fn, out), _p(d_status), _s(stream)))
 
@@ -260,8 +262,8 @@ def mxfp4_matmul_grouped(a_q, a_s, offsets, b_q, b_s, out, alpha: float = 1.0, d
     offsets [E+1]; rows in no group are left as they were."""
     fn = "mxfp4_matmul_grouped"
     (S, N), K, E = out.shape, 2 * a_q.shape[-1], offsets.numel() - 1
-    _sizes(fn, _mx_ok(a_q, a_s, K) and _mx_ok(b_q, b_s, K) and tuple(a_q.shape[:-1]) == (S,)
-           and tuple(b_q.shape[:-1]) == (E, N) and offsets.element_size() == 4)
+    _sizes(fn, _mx_ok(a_q, a_s, (S,), K) and _mx_ok(b_q, b_s, (E, N), K)
+           and offsets.element_size() == 4)
     _check(fn, lib.mxfp4_matmul_grouped(_p(a_q), _p(a_s), _p(offsets), E, _p(b_q), _p(b_s), S, N, K,
                                         float(alpha), _p(out), _out_type(fn, out), _p(d_status),
                                         _s(stream)))
@@ -273,9 +275,8 @@ def mxfp4_matmul_grouped_wgrad(a_q, a_s, b_q, b_s, offsets, out, alpha: float = 
     B [N, P] (mxfp4_quantize_transposed_grouped's outputs for the same offsets)."""
     fn = "mxfp4_matmul_grouped_wgrad"
     (E, M, N), P = out.shape, 2 * a_q.shape[-1]
-    _sizes(fn, _mx_ok(a_q, a_s, P) and _mx_ok(b_q, b_s, P) and tuple(a_q.shape[:-1]) == (M,)
-           and tuple(b_q.shape[:-1]) == (N,) and offsets.numel() == E + 1
-           and offsets.element_size() == 4)
+    _sizes(fn, _mx_ok(a_q, a_s, (M,), P) and _mx_ok(b_q, b_s, (N,), P)
+           and offsets.numel() == E + 1 and offsets.element_size() == 4)
     _check(fn, lib.mxfp4_matmul_grouped_wgrad(_p(a_q), _p(a_s), _p(b_q), _p(b_s), _p(offsets), E, M,
                                               N, P, float(alpha), _p(out), _out_type(fn, out),
                                               _p(d_status), _s(stream)))

@@ -17,6 +17,9 @@
 // warp's stores are contiguous with no staging, and a decode batch of a few
 // rows costs the tensor core only those rows.
 //
+// With few tiles a cluster of CTAs shares each one's k range; the partial sums
+// meet in shared memory and are added in rank order.
+//
 // Persistent, one CTA per SM (two for the narrow tiles).  Warp roles:
 //   warp 0      producer: per stage of 256 k, 128 x 128 bytes of B codes and
 //               NT x 128 bytes of A codes by TMA (zeros past the ends)
@@ -67,6 +70,22 @@ __host__ __device__ constexpr int stages(int NT) {
 }
 __host__ __device__ constexpr int smem_bytes(int NT) {
   return 1024 + stages(NT) * stage_bytes(NT) + kChunkSlots * kChunkBytes + kTableBytes + 512;
+}
+
+// Columns [c0, c1) of the accumulator as fp32 into shared memory, [column][lane].
+__device__ __forceinline__ void stage_columns(uint32_t acc, const Work& w, float* to, int x, int c0, int c1) {
+  for (int c = c0; c < c1; c += 16) {
+    uint32_t r[16];
+    if (w.steps > 0) {
+      tc::tmem_ld16(acc + c, r);
+      tc::tmem_ld_wait();
+    } else {
+#pragma unroll
+      for (int k = 0; k < 16; ++k) r[k] = 0u;
+    }
+#pragma unroll
+    for (int k = 0; k < 16; ++k) to[(c + k) * BX + x] = __uint_as_float(r[k]);
+  }
 }
 
 template <int NT>
@@ -121,6 +140,20 @@ __global__ void __launch_bounds__(threads(NT), ctas_per_sm(NT))
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   const uint32_t n_work = tiles(a, grp);
+  // with a split, the CTAs of a cluster take one tile, each its share of k
+  const uint32_t split = static_cast<uint32_t>(a.split);
+  const uint32_t rank = split > 1 ? tc::cluster_rank() : 0u;
+  const uint32_t first = blockIdx.x / split, stride = gridDim.x / split;
+  const auto next_work = [&](uint32_t i, int& e) {
+    Work w = work_of<NT, STEP, BX>(a, grp, i, e);
+    if (split > 1) {
+      const int nst = stages_of(w);
+      const int s0 = static_cast<int>(rank) * nst / a.split, s1 = static_cast<int>(rank + 1) * nst / a.split;
+      w.k0 += s0 * kStepsPerStage * 64;
+      w.steps = min(w.steps - s0 * kStepsPerStage, (s1 - s0) * kStepsPerStage);
+    }
+    return w;
+  };
   const int ks = static_cast<int>(a.K / 32);
   int ge = 0;  // this role's cursor over the groups
 
@@ -128,8 +161,8 @@ __global__ void __launch_bounds__(threads(NT), ctas_per_sm(NT))
     // ------------------------------------------------------------ producer
     uint32_t s = 0, phase = 0, issued = 0;
     bool ok = true;
-    for (uint32_t i = blockIdx.x; ok && i < n_work; i += gridDim.x) {
-      const Work w = work_of<NT, STEP, BX>(a, grp, i, ge);
+    for (uint32_t i = first; ok && i < n_work; i += stride) {
+      const Work w = next_work(i, ge);
       const int nst = stages_of(w);
       for (int st = 0; st < nst; ++st) {
         if (issued >= NS && !all_wait(&empty[s], phase ^ 1u, abort_flag, a.status)) {
@@ -161,8 +194,8 @@ __global__ void __launch_bounds__(threads(NT), ctas_per_sm(NT))
     uint32_t ch = 0, it = 0, s = 0, phase = 0, g = 0;
     uint32_t old = 0, old_phase = 0;  // ring slot of stage g - 2
     bool ok = true;
-    for (uint32_t i = blockIdx.x; ok && i < n_work; i += gridDim.x, ++it) {
-      const Work w = work_of<NT, STEP, BX>(a, grp, i, ge);
+    for (uint32_t i = first; ok && i < n_work; i += stride, ++it) {
+      const Work w = next_work(i, ge);
       const uint32_t idesc = tc::idesc_mxf4(BX, (w.ny + STEP - 1) & ~(STEP - 1));
       const uint32_t d = tmem + (it & 1) * ACC;
       // accumulator it & 1 was last used by tile it - 2
@@ -241,8 +274,8 @@ __global__ void __launch_bounds__(threads(NT), ctas_per_sm(NT))
     const int blk = (warp - 2) & 1;
     uint32_t ch = 0;
     bool ok = true;
-    for (uint32_t i = blockIdx.x; ok && i < n_work; i += gridDim.x) {
-      const Work w = work_of<NT, STEP, BX>(a, grp, i, ge);
+    for (uint32_t i = first; ok && i < n_work; i += stride) {
+      const Work w = next_work(i, ge);
       const ScaleBlock b = scale_block(a, w, blk, w.x0, ks);
       const int nch = chunks_of(w);
       for (int q = 0; q < nch; ++q, ++ch) {
@@ -264,8 +297,8 @@ __global__ void __launch_bounds__(threads(NT), ctas_per_sm(NT))
     const int part = (warp - kEpi0) >> 2;
     const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
     uint32_t it = 0;
-    for (uint32_t i = blockIdx.x; i < n_work; i += gridDim.x, ++it) {
-      const Work w = work_of<NT, STEP, BX>(a, grp, i, ge);
+    for (uint32_t i = first; i < n_work; i += stride, ++it) {
+      const Work w = next_work(i, ge);
       const uint32_t b = it & 1;
       if (!warp_wait(&dfull[b], (it >> 1) & 1, abort_flag, a.status, 100)) break;
       tc::tc_fence_after();
@@ -275,7 +308,10 @@ __global__ void __launch_bounds__(threads(NT), ctas_per_sm(NT))
       const int all = (w.ny + 15) & ~15;
       const int half = kEpi == 8 ? (all / 2 + 31) & ~31 : all;
       const int c0 = part ? min(half, all) : 0, c1 = part ? all : min(half, all);
-      store_columns(acc, a, w, n, c0, c1);
+      if (split == 1)
+        store_columns(acc, a, w, n, c0, c1);
+      else
+        stage_columns(acc, w, reinterpret_cast<float*>(smem), q * 32 + lane, c0, c1);
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&dempty[b]);
@@ -284,6 +320,31 @@ __global__ void __launch_bounds__(threads(NT), ctas_per_sm(NT))
 
   tc::tc_fence_before();
   __syncthreads();
+  if (split > 1) {
+    // every CTA's share of the sum lies in its ring's memory (its MMAs are done
+    // with it); the columns are shared out and each is added up in rank order
+    tc::cluster_sync();
+    if (first < n_work && *abort_flag == 0) {
+      int e = 0;
+      const Work w = work_of<NT, STEP, BX>(a, grp, first, e);
+      // 256 of the threads: two columns of 128 at a time
+      const int x = threadIdx.x % BX;
+      for (int c = static_cast<int>(rank) * 2 + static_cast<int>(threadIdx.x) / BX;
+           threadIdx.x < 2 * BX && c < w.ny; c += 2 * a.split) {
+        float v = 0.f;
+        for (uint32_t r = 0; r < split; ++r)
+          v += tc::ld_cluster_f32(tc::cluster_addr(smem, r) + static_cast<uint32_t>(c * BX + x) * 4);
+        const int64_t n = static_cast<int64_t>(w.x0) + x, at = (w.out_row + c) * a.x_rows + n;
+        if (n < a.x_rows) {
+          if (a.out_f32)
+            static_cast<float*>(a.out)[at] = a.alpha * v;
+          else
+            static_cast<uint16_t*>(a.out)[at] = static_cast<uint16_t>(cvt_bf16x2(a.alpha * v, 0.f));
+        }
+      }
+    }
+    tc::cluster_sync();  // no CTA leaves while another reads its share
+  }
   if (warp == 1) {
     if (lane == 0) tc::mbar_drain(drain, 0, kWaitLimitNs / 8);
     __syncwarp();
@@ -317,9 +378,31 @@ moe_status launch_nt(Args a, const uint8_t* xq, const uint8_t* yq, cudaStream_t 
   if (!encode_codes(&mx, xq, a.K / 2, a.x_rows, a.mode == kGrouped ? a.E : 1, BX) ||
       !encode_codes(&my, yq, a.K / 2, a.y_rows, 1, NT))
     return MOE_ERR_CUDA;
-  const int64_t cap = static_cast<int64_t>(sm_count()) * ctas_per_sm(NT);
-  const dim3 grid(static_cast<unsigned>(max_work < cap ? max_work : cap));
-  return launch(mxfp4_matmul_kernel<NT>, grid, dim3(threads(NT)), smem_bytes(NT), stream, mx, my, a);
+  // Few tiles leave most SMs without one: a cluster of up to 8 CTAs shares each
+  // tile's k range, as long as a CTA keeps two stages of it.
+  const int64_t sms = sm_count(), nst = (a.K + kStepsPerStage * 64 - 1) / (kStepsPerStage * 64);
+  int64_t split = sms / max_work;
+  if (split > nst / 2) split = nst / 2;
+  if (split > 8) split = 8;
+  a.split = split < 2 ? 1 : static_cast<int>(split);
+  const int64_t cap = sms * ctas_per_sm(NT);
+  const int64_t ctas = a.split > 1 ? max_work * a.split : (max_work < cap ? max_work : cap);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(threads(NT));
+  cfg.dynamicSmemBytes = smem_bytes(NT);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(a.split);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.split > 1 ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, mxfp4_matmul_kernel<NT>, mx, my, a) != cudaSuccess) {
+    cudaGetLastError();
+    return MOE_ERR_CUDA;
+  }
+  return MOE_OK;
 }
 
 // Rows of A per tile: `rows` is what one tile may meet, twice the mean of a

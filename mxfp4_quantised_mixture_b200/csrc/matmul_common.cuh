@@ -29,6 +29,7 @@ enum Mode : int { kDense = 0, kGrouped = 1, kWgrad = 2 };
 struct Args {
   int mode, E;
   FastDiv xt, yt;          // tiles along B's rows, and along A's
+  int split;               // CTAs of a cluster that share a tile's k range, 1 for none
   const int32_t* offsets;  // grouped, wgrad
   const uint8_t* xs;       // scales of B, [rows][ks]
   const uint8_t* ys;       // scales of A, [rows][ks]
