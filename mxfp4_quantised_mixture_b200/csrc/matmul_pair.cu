@@ -55,7 +55,7 @@ constexpr int SPC = kStagesPerChunk / WPS;   // stages per scale chunk
 constexpr int kWriters = 4, kEpi = 8;  // warps (writers: per group)
 constexpr int kWriter0 = 4, kEpi0 = 12;
 constexpr int kThreads = 32 * (kEpi0 + kEpi);
-constexpr int kRowsAtOnce = 21;  // rows of scales the two loader warps take at once
+constexpr int kRowsAtOnce = 16;  // rows of scales the two loader warps take at once
 // a scale chunk in shared memory: of every row the three aligned 16-byte pieces
 // that cover its 32 bytes
 constexpr int kRowBytes = 48, kRows = 128 + NT;
@@ -254,8 +254,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // -------------------------------------------------------- scale loaders
     // Three threads to a row, one per piece; a piece's bytes past its row's end
     // (or the array's) are not read and become 0, as their codes are.
+    // A thread's rows are 16 apart, so one misalignment holds for all of them and
+    // a copy takes five instructions.  (At any other distance it took 25, and the
+    // loaders' own instructions held the products back.)
     const int lt = (warp - 2) * 32 + lane;
-    const int r0 = lt / 3, piece = lt % 3;  // the 64th thread has none
+    const int r0 = lt / 3, piece = lt % 3;  // 48 of the 64 threads have one
+    const int64_t pitch = static_cast<int64_t>(kRowsAtOnce) * ks;
     uint32_t slot = 0, phase = 0, ch = 0;
     bool ok = true;
     for (uint32_t i = first; ok && i < n_work; i += stride) {
@@ -265,25 +269,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int xr = static_cast<int>(min(a.x_rows - x0, static_cast<int64_t>(128)));
       const uint8_t* px = a.xs + (x0 + (a.mode == kGrouped ? w.e * a.x_rows : 0) + r0) * ks + w.k0 / 32;
       const uint8_t* py = a.ys + (static_cast<int64_t>(w.y0) + r0) * ks + w.k0 / 32;
+      const int mx = static_cast<int>(reinterpret_cast<uintptr_t>(px) & 15u);
+      const int my = static_cast<int>(reinterpret_cast<uintptr_t>(py) & 15u);
+      px += 16 * piece - mx;
+      py += 16 * piece - my;
       for (int q = 0; q < nch; ++q, ++ch) {
         if (ch >= kSlots && !warp_wait(&sempty[slot], phase ^ 1u, abort_flag, a.status, 50)) {
           ok = false;
           break;
         }
         const int byte = q * kWords * 4, n = min(32, left - byte);
+        const int bx = max(0, min(16, mx + n - 16 * piece)), by = max(0, min(16, my + n - 16 * piece));
         const uint32_t dst = tc::smem_u32(chunks + slot * kChunkBytes) + r0 * kRowBytes + piece * 16;
-        const auto move = [&](const uint8_t* p, int row, int rows, int block) {
-          const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u);
-          const int bytes = row < rows ? max(0, min(16, mis + n - 16 * piece)) : 0;
-          tc::cp_async16(dst + (block + row - r0) * kRowBytes, bytes ? p - mis + 16 * piece : a.xs, bytes);
-        };
         if (r0 < kRowsAtOnce) {
+          // of an absent row or piece nothing is read: its size is 0
+          const uint8_t* p = px + byte;
 #pragma unroll
-          for (int j = 0; j < 128; j += kRowsAtOnce)
-            if (r0 + j < 128) move(px + j * ks + byte, r0 + j, xr, 0);
+          for (int j = 0; j < 128; j += kRowsAtOnce) {
+            const bool in = r0 + j < xr && bx > 0;
+            tc::cp_async16(dst + j * kRowBytes, in ? p : a.xs, in ? bx : 0);
+            p += pitch;
+          }
+          p = py + byte;
 #pragma unroll
-          for (int j = 0; j < NT; j += kRowsAtOnce)
-            if (r0 + j < NT) move(py + j * ks + byte, r0 + j, w.ny, 128);
+          for (int j = 0; j < NT; j += kRowsAtOnce) {
+            const bool in = r0 + j < w.ny && by > 0;
+            tc::cp_async16(dst + (128 + j) * kRowBytes, in ? p : a.ys, in ? by : 0);
+            p += pitch;
+          }
         }
         tc::cp_async_arrive(&sfull[slot]);
         if (++slot == kSlots) {
