@@ -186,11 +186,50 @@ def mxfp4_quantize_sr_rht(w_bf16, flags: int, rht_signs, seed: int, q_packed, sc
                                      _p(d_status), _s(stream)))
 
 
+def _ptrs(fn: str, *tensors) -> list:
+    """Device pointers of a call's tensors, which have to live on the current
+    device (its stream runs the call) and to be dense; None passes through."""
+    import torch
+
+    dev, out = torch.cuda.current_device() if torch.cuda.is_initialized() else None, []
+    for t in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{fn}: tensor arguments must live on a CUDA device")
+        if t.get_device() != dev:
+            raise ValueError(f"{fn}: tensor arguments must live on the current device")
+        if not t.is_contiguous():
+            raise ValueError(f"{fn}: tensor arguments must be contiguous (dense row-major)")
+        out.append(t.data_ptr())
+    return out
+
+
 def _sizes(fn: str, ok: bool) -> None:
     """Shapes that contradict one another are refused before the C call, which
     would otherwise read or write past the smaller one."""
     if not ok:
         raise ValueError(f"{fn}: the tensors' shapes or types do not belong together")
+
+
+def _is_i32(t) -> bool:
+    import torch
+
+    return t.dtype is torch.int32
+
+
+def _is_f32(t) -> bool:
+    import torch
+
+    return t.dtype is torch.float32
+
+
+def _is_bf16(t) -> bool:
+    """bfloat16, or 16-bit integers that carry its bits."""
+    import torch
+
+    return t.dtype in (torch.bfloat16, torch.int16, torch.uint16)
 
 
 def _out_type(fn: str, out) -> int:
@@ -225,11 +264,11 @@ def mxfp4_quantize_transposed(w_bf16, q_packed, scales, d_status=None, stream=No
     fn = "mxfp4_quantize_transposed"
     R, C = w_bf16.shape[-2:]
     P = mxfp4_transposed_width(R)
-    _sizes(fn, w_bf16.element_size() == 2
+    _sizes(fn, _is_bf16(w_bf16)
            and _mx_ok(q_packed, scales, tuple(w_bf16.shape[:-2]) + (C,), P))
     batch = w_bf16.numel() // (R * C) if R * C else 0
-    _check(fn, lib.mxfp4_quantize_transposed(_p(w_bf16), batch, R, C, _p(q_packed), _p(scales),
-                                             _p(d_status), _s(stream)))
+    w, q, sc, st = _ptrs(fn, w_bf16, q_packed, scales, d_status)
+    _check(fn, lib.mxfp4_quantize_transposed(w, batch, R, C, q, sc, st, _s(stream)))
 
 
 def mxfp4_quantize_transposed_grouped(w_bf16, offsets, q_packed, scales, d_status=None,
@@ -240,11 +279,10 @@ def mxfp4_quantize_transposed_grouped(w_bf16, offsets, q_packed, scales, d_statu
     S, C = w_bf16.shape
     E = offsets.numel() - 1
     P = mxfp4_transposed_width(S, E)
-    _sizes(fn, w_bf16.element_size() == 2 and offsets.element_size() == 4
+    _sizes(fn, _is_bf16(w_bf16) and _is_i32(offsets)
            and _mx_ok(q_packed, scales, (C,), P))
-    _check(fn, lib.mxfp4_quantize_transposed_grouped(_p(w_bf16), S, C, _p(offsets), E,
-                                                     _p(q_packed), _p(scales), _p(d_status),
-                                                     _s(stream)))
+    w, off, q, sc, st = _ptrs(fn, w_bf16, offsets, q_packed, scales, d_status)
+    _check(fn, lib.mxfp4_quantize_transposed_grouped(w, S, C, off, E, q, sc, st, _s(stream)))
 
 
 def mxfp4_matmul(a_q, a_s, b_q, b_s, out, alpha: float = 1.0, d_status=None, stream=None) -> None:
@@ -252,8 +290,9 @@ def mxfp4_matmul(a_q, a_s, b_q, b_s, out, alpha: float = 1.0, d_status=None, str
     fn = "mxfp4_matmul"
     (M, N), K = out.shape, 2 * a_q.shape[-1]
     _sizes(fn, _mx_ok(a_q, a_s, (M,), K) and _mx_ok(b_q, b_s, (N,), K))
-    _check(fn, lib.mxfp4_matmul(_p(a_q), _p(a_s), _p(b_q), _p(b_s), M, N, K, float(alpha), _p(out),
-                                _out_type(fn, out), _p(d_status), _s(stream)))
+    kind = _out_type(fn, out)
+    aq, sa, bq, sb, o, st = _ptrs(fn, a_q, a_s, b_q, b_s, out, d_status)
+    _check(fn, lib.mxfp4_matmul(aq, sa, bq, sb, M, N, K, float(alpha), o, kind, st, _s(stream)))
 
 
 def mxfp4_matmul_grouped(a_q, a_s, offsets, b_q, b_s, out, alpha: float = 1.0, d_status=None,
@@ -263,9 +302,10 @@ def mxfp4_matmul_grouped(a_q, a_s, offsets, b_q, b_s, out, alpha: float = 1.0, d
     fn = "mxfp4_matmul_grouped"
     (S, N), K, E = out.shape, 2 * a_q.shape[-1], offsets.numel() - 1
     _sizes(fn, _mx_ok(a_q, a_s, (S,), K) and _mx_ok(b_q, b_s, (E, N), K)
-           and offsets.element_size() == 4)
-    _check(fn, lib.mxfp4_matmul_grouped(_p(a_q), _p(a_s), _p(offsets), E, _p(b_q), _p(b_s), S, N, K,
-                                        float(alpha), _p(out), _out_type(fn, out), _p(d_status),
+           and _is_i32(offsets))
+    kind = _out_type(fn, out)
+    aq, sa, off, bq, sb, o, st = _ptrs(fn, a_q, a_s, offsets, b_q, b_s, out, d_status)
+    _check(fn, lib.mxfp4_matmul_grouped(aq, sa, off, E, bq, sb, S, N, K, float(alpha), o, kind, st,
                                         _s(stream)))
 
 
@@ -276,10 +316,11 @@ def mxfp4_matmul_grouped_wgrad(a_q, a_s, b_q, b_s, offsets, out, alpha: float = 
     fn = "mxfp4_matmul_grouped_wgrad"
     (E, M, N), P = out.shape, 2 * a_q.shape[-1]
     _sizes(fn, _mx_ok(a_q, a_s, (M,), P) and _mx_ok(b_q, b_s, (N,), P)
-           and offsets.numel() == E + 1 and offsets.element_size() == 4)
-    _check(fn, lib.mxfp4_matmul_grouped_wgrad(_p(a_q), _p(a_s), _p(b_q), _p(b_s), _p(offsets), E, M,
-                                              N, P, float(alpha), _p(out), _out_type(fn, out),
-                                              _p(d_status), _s(stream)))
+           and offsets.numel() == E + 1 and _is_i32(offsets))
+    kind = _out_type(fn, out)
+    aq, sa, bq, sb, off, o, st = _ptrs(fn, a_q, a_s, b_q, b_s, offsets, out, d_status)
+    _check(fn, lib.mxfp4_matmul_grouped_wgrad(aq, sa, bq, sb, off, E, M, N, P, float(alpha), o, kind,
+                                              st, _s(stream)))
 
 
 def moe_route(logits, k: int, topk_idx, topk_w, stream=None) -> None:
@@ -342,18 +383,27 @@ def moe_combine_backward(dout, y_perm, slot_pos, topk_w, shape: moe_shape, dy_pe
                          dscore=None, stream=None) -> None:
     """Gradients of moe_combine: dy_perm [S][D], dtopk_w [T][k], and dscore [T][k] of the
     k chosen logits through the softmax (the last two when given)."""
-    _check("moe_combine_backward",
-           lib.moe_combine_backward(_p(dout), _p(y_perm), _p(slot_pos), _p(topk_w), shape,
-                                    _p(dy_perm), _p(dtopk_w), _p(dscore), _s(stream)))
+    fn, T, k, D = "moe_combine_backward", shape.T, shape.k, shape.d_model
+    _sizes(fn, _is_bf16(dout) and dout.shape == (T, D) and _is_bf16(dy_perm) and dy_perm.shape == (T * k, D)
+           and _is_i32(slot_pos) and slot_pos.numel() == T * k
+           and (y_perm is None or (_is_bf16(y_perm) and y_perm.shape == (T * k, D)))
+           and all(t is None or (_is_f32(t) and t.shape == (T, k)) for t in (topk_w, dtopk_w, dscore)))
+    g, y, pos, w, dy, dw, ds = _ptrs(fn, dout, y_perm, slot_pos, topk_w, dy_perm, dtopk_w, dscore)
+    _check(fn, lib.moe_combine_backward(g, y, pos, w, shape, dy, dw, ds, _s(stream)))
 
 
 def moe_permute_backward(dx_perm, slot_pos, shape: moe_shape, dx, topk_idx=None, dscore=None,
                          w_router=None, stream=None) -> None:
     """Gradient of moe_permute's gather: dx [T][D], plus the router's share when
     topk_idx [T][k], dscore [T][k] and w_router [E][D] are given."""
-    _check("moe_permute_backward",
-           lib.moe_permute_backward(_p(dx_perm), _p(slot_pos), shape, _p(dx), _p(topk_idx),
-                                    _p(dscore), _p(w_router), _s(stream)))
+    fn, T, k, D = "moe_permute_backward", shape.T, shape.k, shape.d_model
+    _sizes(fn, _is_bf16(dx_perm) and dx_perm.shape == (T * k, D) and _is_bf16(dx) and dx.shape == (T, D)
+           and _is_i32(slot_pos) and slot_pos.numel() == T * k
+           and (topk_idx is None or (_is_i32(topk_idx) and topk_idx.shape == (T, k)))
+           and (dscore is None or (_is_f32(dscore) and dscore.shape == (T, k)))
+           and (w_router is None or (_is_bf16(w_router) and w_router.shape == (shape.E, D))))
+    g, pos, o, idx, ds, wr = _ptrs(fn, dx_perm, slot_pos, dx, topk_idx, dscore, w_router)
+    _check(fn, lib.moe_permute_backward(g, pos, shape, o, idx, ds, wr, _s(stream)))
 
 
 def moe_layer_forward(x, logits, shape: moe_shape, wgu_q, wgu_s, wdn_q, wdn_s, out, ws,

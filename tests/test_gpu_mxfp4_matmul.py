@@ -254,3 +254,54 @@ def test_streams_and_graphs(cuda_device):
     torch.cuda.synchronize()
     for a, b, out in sides:
         assert_product(out, value(*a), value(*b), 512, 1.0)
+
+
+def test_outputs_past_32_bits(cuda_device):
+    # 2^30 < 40000 * 30016 elements, past 2^32 bytes: rows from the start, the middle and the end
+    gen = generator(cuda_device, 13)
+    M, N, K = 40000, 30016, 64
+    a, b = random_mx(gen, (M, K)), random_mx(gen, (N, K))
+    out = torch.empty((M, N), device=cuda_device)
+    moe.mxfp4_matmul(*a, *b, out)
+    for lo in (0, 17777, M - 33):
+        rows = slice(lo, lo + 33)
+        assert_product(out[rows], value(a[0][rows], a[1][rows]), value(*b), K, 1.0)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 2880, 2880), (16, 256, 4096), (100, 130, 16384), (33, 300, 1088)])
+def test_few_tiles_share_the_contraction(cuda_device, M, N, K):
+    # a cluster of CTAs splits k; the outcome is the same on every call, and the empty sum of a
+    # group without positions is zero there too
+    gen = generator(cuda_device, M + K)
+    a, b = random_mx(gen, (M, K)), random_mx(gen, (N, K))
+    outs = []
+    for _ in range(5):
+        out, whole = guarded((M, N), torch.float32, cuda_device, FILL)
+        moe.mxfp4_matmul(*a, *b, out, alpha=2.0)
+        assert behind_untouched(out, whole, FILL)
+        outs.append(out)
+    assert_product(outs[0], value(*a), value(*b), K, 2.0)
+    assert all(torch.equal(o, outs[0]) for o in outs)
+
+
+def test_wgrad_with_few_tiles(cuda_device):
+    counts, M, N = [0, 3000, 70], 24, 130
+    S, E = sum(counts), len(counts)
+    gen = generator(cuda_device, 14)
+    off = offsets_of(counts, cuda_device)
+    P = moe.mxfp4_transposed_width(S, E)
+    pair = []
+    for C in (M, N + 6):
+        q = torch.empty((C, P // 2), dtype=torch.uint8, device=cuda_device)
+        s = torch.empty((C, P // 32), dtype=torch.uint8, device=cuda_device)
+        w = torch.randn((S, C), generator=gen, device=cuda_device).to(torch.bfloat16)
+        moe.mxfp4_quantize_transposed_grouped(w, off, q, s)
+        pair.append((q[:C - 6 * (C != M)].contiguous(), s[:C - 6 * (C != M)].contiguous()))
+    out = torch.full((E, M, N), FILL, device=cuda_device)
+    moe.mxfp4_matmul_grouped_wgrad(*pair[0], *pair[1], off, out)
+    p = 0
+    for e, c in enumerate(counts):
+        n = (c + 127) // 128 * 128
+        a, b = (value(q[:, p // 2:(p + n) // 2], s[:, p // 32:(p + n) // 32]) for q, s in pair)
+        assert_product(out[e], a, b, max(n, 1), 1.0)
+        p += n

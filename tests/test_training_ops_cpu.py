@@ -119,6 +119,30 @@ def test_binding_refuses_shapes_that_contradict():
                                               u8(16, 32), u8(16, 2))
 
 
+def test_binding_refuses_gradient_shapes_that_contradict():
+    sh = moe.make_shape(4, 8, 2, 128, 128)
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+    pos, w = torch.zeros(8, dtype=torch.int32), torch.zeros((4, 2))
+    good = [bf(4, 128), bf(8, 128), pos, w, sh, bf(8, 128), w, w]
+    for i, wrong in [(0, bf(5, 128)), (1, bf(4, 128)), (2, pos[:7]), (3, torch.zeros((2, 4))),
+                     (5, bf(8, 64)), (6, torch.zeros((4, 3))), (2, pos.long())]:
+        args = list(good)
+        args[i] = wrong
+        with pytest.raises(ValueError, match="belong together"):
+            moe.moe_combine_backward(*args)
+    with pytest.raises(ValueError, match="CUDA device"):
+        moe.moe_combine_backward(*good)
+    good = [bf(8, 128), pos, sh, bf(4, 128), torch.zeros((4, 2), dtype=torch.int32), w, bf(8, 128)]
+    for i, wrong in [(0, bf(4, 128)), (1, pos.float()), (3, bf(4, 64)), (4, pos), (5, torch.zeros((4, 1))),
+                     (6, bf(7, 128))]:
+        args = list(good)
+        args[i] = wrong
+        with pytest.raises(ValueError, match="belong together"):
+            moe.moe_permute_backward(*args)
+    with pytest.raises(ValueError, match="CUDA device"):
+        moe.moe_permute_backward(*good)
+
+
 def test_well_formed_calls_fail_cleanly_without_a_device():
     if torch.cuda.is_available():
         pytest.skip("its placeholder pointers must never reach a device")
