@@ -327,19 +327,33 @@ __global__ void __launch_bounds__(threads(NT), ctas_per_sm(NT))
     if (first < n_work && *abort_flag == 0) {
       int e = 0;
       const Work w = work_of<NT, STEP, BX>(a, grp, first, e);
-      // 256 of the threads: two columns of 128 at a time
-      const int x = threadIdx.x % BX;
-      for (int c = static_cast<int>(rank) * 2 + static_cast<int>(threadIdx.x) / BX;
-           threadIdx.x < 2 * BX && c < w.ny; c += 2 * a.split) {
-        float v = 0.f;
-        for (uint32_t r = 0; r < split; ++r)
-          v += tc::ld_cluster_f32(tc::cluster_addr(smem, r) + static_cast<uint32_t>(c * BX + x) * 4);
-        const int64_t n = static_cast<int64_t>(w.x0) + x, at = (w.out_row + c) * a.x_rows + n;
-        if (n < a.x_rows) {
+      // 32 threads to a column of 128, four neighbours each
+      constexpr int kCols = threads(NT) / 32;
+      const int x = lane * 4;
+      const int64_t n = static_cast<int64_t>(w.x0) + x;
+      for (int c = static_cast<int>(rank) * kCols + warp; c < w.ny; c += kCols * a.split) {
+        float4 part[8];
+        const uint32_t off = static_cast<uint32_t>(c * BX + x) * 4;
+#pragma unroll
+        for (uint32_t r = 0; r < 8; ++r)
+          part[r] = r < split ? tc::ld_cluster_f32x4(tc::cluster_addr(smem, r) + off)
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          v[0] += part[r].x;
+          v[1] += part[r].y;
+          v[2] += part[r].z;
+          v[3] += part[r].w;
+        }
+        const int64_t at = (w.out_row + c) * a.x_rows + n;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (n + k >= a.x_rows) break;
           if (a.out_f32)
-            static_cast<float*>(a.out)[at] = a.alpha * v;
+            static_cast<float*>(a.out)[at + k] = a.alpha * v[k];
           else
-            static_cast<uint16_t*>(a.out)[at] = static_cast<uint16_t>(cvt_bf16x2(a.alpha * v, 0.f));
+            static_cast<uint16_t*>(a.out)[at + k] = static_cast<uint16_t>(cvt_bf16x2(a.alpha * v[k], 0.f));
         }
       }
     }
@@ -354,6 +368,38 @@ __global__ void __launch_bounds__(threads(NT), ctas_per_sm(NT))
 }
 
 // ------------------------------------------------------------ host helpers
+
+struct ClusterLaunch {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1] = {};
+  ClusterLaunch(unsigned grid, int block, int smem, int cluster, cudaStream_t stream) {
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 1 : 0;
+  }
+};
+
+// How many clusters of `size` CTAs the device runs at a time (asked once).
+template <int NT>
+int clusters_at_once(int dev, int size) {
+  static std::atomic<int> known[64][9];
+  const bool keep = dev >= 0 && dev < 64;
+  int n = keep ? known[dev][size].load() - 1 : -1;
+  if (n >= 0) return n;
+  ClusterLaunch l(static_cast<unsigned>(size), threads(NT), smem_bytes(NT), size, nullptr);
+  if (cudaOccupancyMaxActiveClusters(&n, mxfp4_matmul_kernel<NT>, &l.cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  if (keep) known[dev][size].store(n + 1);
+  return n;
+}
 
 template <int NT>
 moe_status launch_nt(Args a, const uint8_t* xq, const uint8_t* yq, cudaStream_t stream) {
@@ -379,25 +425,18 @@ moe_status launch_nt(Args a, const uint8_t* xq, const uint8_t* yq, cudaStream_t 
       !encode_codes(&my, yq, a.K / 2, a.y_rows, 1, NT))
     return MOE_ERR_CUDA;
   // Few tiles leave most SMs without one: a cluster of up to 8 CTAs shares each
-  // tile's k range, as long as a CTA keeps two stages of it.
+  // tile's k range, as long as a CTA keeps two stages of it and all the clusters
+  // run at once (23 clusters of 6 do not: 22 fit, and the last would wait).
   const int64_t sms = sm_count(), nst = (a.K + kStepsPerStage * 64 - 1) / (kStepsPerStage * 64);
   int64_t split = sms / max_work;
   if (split > nst / 2) split = nst / 2;
   if (split > 8) split = 8;
+  while (split > 1 && clusters_at_once<NT>(dev, static_cast<int>(split)) < max_work) --split;
   a.split = split < 2 ? 1 : static_cast<int>(split);
   const int64_t cap = sms * ctas_per_sm(NT);
   const int64_t ctas = a.split > 1 ? max_work * a.split : (max_work < cap ? max_work : cap);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-  cfg.blockDim = dim3(threads(NT));
-  cfg.dynamicSmemBytes = smem_bytes(NT);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(a.split);
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = a.split > 1 ? 1 : 0;
+  ClusterLaunch l(static_cast<unsigned>(ctas), threads(NT), smem_bytes(NT), a.split, stream);
+  const cudaLaunchConfig_t& cfg = l.cfg;
   if (cudaLaunchKernelEx(&cfg, mxfp4_matmul_kernel<NT>, mx, my, a) != cudaSuccess) {
     cudaGetLastError();
     return MOE_ERR_CUDA;
