@@ -445,9 +445,15 @@ moe_status launch_nt(Args a, const uint8_t* xq, const uint8_t* yq, cudaStream_t 
 }
 
 // Rows of A per tile: `rows` is what one tile may meet, twice the mean of a
-// group where there are groups.
+// group where there are groups.  More than 128 take the CTA pairs, unless so few
+// 128 x 128 tiles come of it that three CTAs and more can share each one's k:
+// 300 x 300 x 16384 then takes 13 us instead of 26, 1000 x 600 x 8192 15 instead
+// of 18, while 512 x 2880 x 8192, at 92 tiles, takes 21 instead of 18.5.
 moe_status run(Args a, const uint8_t* xq, const uint8_t* yq, int64_t rows, cudaStream_t stream) {
-  if (rows > 128 && a.x_rows > 128) return launch_pair(a, xq, yq, stream);
+  if (rows > 128 && a.x_rows > 128) {
+    Args few = a;
+    if (3 * plan_tiles(&few, BX, 128) > sm_count()) return launch_pair(a, xq, yq, stream);
+  }
   const int NT = rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= 64 ? 64 : 128));
   switch (NT) {
     case 16: return launch_nt<16>(a, xq, yq, stream);

@@ -305,3 +305,64 @@ def test_wgrad_with_few_tiles(cuda_device):
         a, b = (value(q[:, p // 2:(p + n) // 2], s[:, p // 32:(p + n) // 32]) for q, s in pair)
         assert_product(out[e], a, b, max(n, 1), 1.0)
         p += n
+
+
+# More than 49 tiles of 128 x 128 run on CTA pairs: widths that fill no tile, odd output widths, k
+# that ends inside every kind of step, one and several scale chunks
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,N,K", [(1500, 1301, 1120), (2000, 1000, 288), (1300, 1300, 32),
+                                   (1100, 1111, 4128), (193, 4100, 544), (6500, 130, 96),
+                                   (1345, 1537, 2080), (900, 1024, 1024)])
+def test_dense_on_pairs(cuda_device, M, N, K, dtype):
+    gen = generator(cuda_device, M + N + K)
+    a, b = random_mx(gen, (M, K)), random_mx(gen, (N, K))
+    out, whole = guarded((M, N), dtype, cuda_device, FILL)
+    st = status(cuda_device)
+    moe.mxfp4_matmul(*a, *b, out, alpha=0.25, d_status=st)
+    assert int(st) == 0
+    assert_product(out, value(*a), value(*b), K, 0.25)
+    assert behind_untouched(out, whole, FILL)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("counts,N,K", [([300, 17, 0, 700, 193, 1], 2050, 1056),
+                                        ([0, 1500, 0], 1301, 160), ([193] * 9, 900, 2880),
+                                        ([5, 3000, 0, 1, 64], 1024, 512)])
+def test_grouped_on_pairs(cuda_device, counts, N, K, dtype):
+    E, S, before, behind = len(counts), sum(counts), 5, 7
+    gen = generator(cuda_device, S + N + K)
+    a, b = random_mx(gen, (before + S + behind, K)), random_mx(gen, (E, N, K))
+    # rows of no group hold NaN scales: no group's rows may meet them
+    a[1][:before] = 255
+    a[1][-behind:] = 255
+    out, whole = guarded((before + S + behind, N), dtype, cuda_device, FILL)
+    moe.mxfp4_matmul_grouped(*a, offsets_of(counts, cuda_device, before), *b, out)
+    av, lo = value(*a), before
+    for e, c in enumerate(counts):
+        if c:
+            assert_product(out[lo:lo + c], av[lo:lo + c], value(b[0][e], b[1][e]), K, 1.0)
+        lo += c
+    assert bool((out[:before] == FILL).all()) and bool((out[-behind:] == FILL).all())
+    assert behind_untouched(out, whole, FILL)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("counts,M,N", [([130, 0, 700, 64], 1000, 1304), ([1, 0], 1200, 800),
+                                        ([2500], 904, 1000), ([64, 65, 63, 0, 1025], 320, 904)])
+def test_wgrad_on_pairs(cuda_device, counts, M, N, dtype):
+    test_wgrad(cuda_device, counts, M, N, dtype)
+
+
+def test_pairs_repeat_bit_for_bit_and_share_the_device(cuda_device):
+    gen = generator(cuda_device, 15)
+    counts = [37, 0, 512, 3, 260, 900]
+    a, b = random_mx(gen, (sum(counts), 1120)), random_mx(gen, (6, 1700, 1120))
+    off = offsets_of(counts, cuda_device)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    outs = [torch.empty((sum(counts), 1700), device=cuda_device) for _ in range(24)]
+    torch.cuda.synchronize()
+    for i, out in enumerate(outs):
+        moe.mxfp4_matmul_grouped(*a, off, *b, out, stream=streams[i % 2])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, outs[0]) for o in outs)
