@@ -186,50 +186,43 @@ def mxfp4_quantize_sr_rht(w_bf16, flags: int, rht_signs, seed: int, q_packed, sc
                                      _p(d_status), _s(stream)))
 
 
-def _ptrs(fn: str, *tensors) -> list:
-    """Device pointers of a call's tensors, which have to live on the current
-    device (its stream runs the call) and to be dense; None passes through."""
+_types: tuple = ()  # (uint8, int32, float32, the 16-bit types that carry bf16), once torch is there
+
+
+def _dtypes() -> tuple:
+    global _types
+    if not _types:
+        import torch
+
+        _types = ((torch.uint8,), (torch.int32,), (torch.float32,),
+                  (torch.bfloat16, torch.int16, torch.uint16))
+    return _types
+
+
+def _args(fn: str, *specs) -> list:
+    """Device pointers of a call's tensors, given as (tensor, shape, types); a
+    tensor that is None passes through.  Shapes or types that contradict one
+    another are refused (the C call would read or write past the smaller one),
+    and so are tensors off the current device, whose stream runs the call, and
+    strided views."""
     import torch
 
-    dev, out = torch.cuda.current_device() if torch.cuda.is_initialized() else None, []
-    for t in tensors:
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else None
+    out, off = [], False
+    for t, shape, types in specs:
         if t is None:
             out.append(None)
             continue
-        if not t.is_cuda:
-            raise ValueError(f"{fn}: tensor arguments must live on a CUDA device")
+        if (shape is not None and t.shape != shape) or t.dtype not in types:
+            raise ValueError(f"{fn}: the tensors' shapes or types do not belong together")
         if t.get_device() != dev:
-            raise ValueError(f"{fn}: tensor arguments must live on the current device")
+            off = True
         if not t.is_contiguous():
             raise ValueError(f"{fn}: tensor arguments must be contiguous (dense row-major)")
         out.append(t.data_ptr())
+    if off:
+        raise ValueError(f"{fn}: tensor arguments must live on a CUDA device, the current one")
     return out
-
-
-def _sizes(fn: str, ok: bool) -> None:
-    """Shapes that contradict one another are refused before the C call, which
-    would otherwise read or write past the smaller one."""
-    if not ok:
-        raise ValueError(f"{fn}: the tensors' shapes or types do not belong together")
-
-
-def _is_i32(t) -> bool:
-    import torch
-
-    return t.dtype is torch.int32
-
-
-def _is_f32(t) -> bool:
-    import torch
-
-    return t.dtype is torch.float32
-
-
-def _is_bf16(t) -> bool:
-    """bfloat16, or 16-bit integers that carry its bits."""
-    import torch
-
-    return t.dtype in (torch.bfloat16, torch.int16, torch.uint16)
 
 
 def _out_type(fn: str, out) -> int:
@@ -242,15 +235,6 @@ def _out_type(fn: str, out) -> int:
     raise ValueError(f"{fn}: the output is bfloat16 or float32, not {out.dtype}")
 
 
-def _mx_ok(q, s, lead: tuple, K: int) -> bool:
-    """Codes and scales of an MXFP4 tensor [*lead, K]."""
-    import torch
-
-    u8 = torch.uint8
-    return (K % 32 == 0 and q.dtype is u8 and s.dtype is u8 and q.shape == lead + (K // 2,)
-            and s.shape == lead + (K // 32,))
-
-
 def mxfp4_transposed_width(rows: int, E: int = 0) -> int:
     """Positions along the contraction axis of a transposed MXFP4 matrix: rows
     rounded up to 32, or, with E groups of rows, room for each of them to start
@@ -261,13 +245,13 @@ def mxfp4_transposed_width(rows: int, E: int = 0) -> int:
 def mxfp4_quantize_transposed(w_bf16, q_packed, scales, d_status=None, stream=None) -> None:
     """w_bf16 [..., R, C] bf16 -> q_packed [..., C, P/2] u8, scales [..., C, P/32] u8,
     P = mxfp4_transposed_width(R): mxfp4_quantize of the transpose."""
-    fn = "mxfp4_quantize_transposed"
-    R, C = w_bf16.shape[-2:]
-    P = mxfp4_transposed_width(R)
-    _sizes(fn, _is_bf16(w_bf16)
-           and _mx_ok(q_packed, scales, tuple(w_bf16.shape[:-2]) + (C,), P))
+    fn, (u8, i32, _, b16) = "mxfp4_quantize_transposed", _dtypes()
+    shape = tuple(w_bf16.shape)
+    R, C = shape[-2:]
+    P, lead = mxfp4_transposed_width(R), shape[:-2] + (C,)
+    w, q, sc, st = _args(fn, (w_bf16, shape, b16), (q_packed, lead + (P // 2,), u8),
+                         (scales, lead + (P // 32,), u8), (d_status, None, i32))
     batch = w_bf16.numel() // (R * C) if R * C else 0
-    w, q, sc, st = _ptrs(fn, w_bf16, q_packed, scales, d_status)
     _check(fn, lib.mxfp4_quantize_transposed(w, batch, R, C, q, sc, st, _s(stream)))
 
 
@@ -275,37 +259,37 @@ def mxfp4_quantize_transposed_grouped(w_bf16, offsets, q_packed, scales, d_statu
                                       stream=None) -> None:
     """w_bf16 [S, C] bf16, offsets [E+1] i32 -> q_packed [C, P/2], scales [C, P/32],
     P = mxfp4_transposed_width(S, E), every group at a multiple of 128 positions."""
-    fn = "mxfp4_quantize_transposed_grouped"
+    fn, (u8, i32, _, b16) = "mxfp4_quantize_transposed_grouped", _dtypes()
     S, C = w_bf16.shape
     E = offsets.numel() - 1
     P = mxfp4_transposed_width(S, E)
-    _sizes(fn, _is_bf16(w_bf16) and _is_i32(offsets)
-           and _mx_ok(q_packed, scales, (C,), P))
-    w, off, q, sc, st = _ptrs(fn, w_bf16, offsets, q_packed, scales, d_status)
+    w, off, q, sc, st = _args(fn, (w_bf16, (S, C), b16), (offsets, (E + 1,), i32),
+                              (q_packed, (C, P // 2), u8), (scales, (C, P // 32), u8),
+                              (d_status, None, i32))
     _check(fn, lib.mxfp4_quantize_transposed_grouped(w, S, C, off, E, q, sc, st, _s(stream)))
 
 
 def mxfp4_matmul(a_q, a_s, b_q, b_s, out, alpha: float = 1.0, d_status=None, stream=None) -> None:
     """out [M, N] (bf16 or fp32) = alpha * A B^T of MXFP4 A [M, K] and B [N, K]."""
-    fn = "mxfp4_matmul"
-    (M, N), K = out.shape, 2 * a_q.shape[-1]
-    _sizes(fn, _mx_ok(a_q, a_s, (M,), K) and _mx_ok(b_q, b_s, (N,), K))
-    kind = _out_type(fn, out)
-    aq, sa, bq, sb, o, st = _ptrs(fn, a_q, a_s, b_q, b_s, out, d_status)
-    _check(fn, lib.mxfp4_matmul(aq, sa, bq, sb, M, N, K, float(alpha), o, kind, st, _s(stream)))
+    fn, (u8, i32, _, _) = "mxfp4_matmul", _dtypes()
+    (M, N), h, kind = out.shape, a_q.shape[-1], _out_type(fn, out)
+    aq, sa, bq, sb, o, st = _args(fn, (a_q, (M, h), u8), (a_s, (M, h // 16), u8), (b_q, (N, h), u8),
+                                  (b_s, (N, h // 16), u8), (out, (M, N), (out.dtype,)),
+                                  (d_status, None, i32))
+    _check(fn, lib.mxfp4_matmul(aq, sa, bq, sb, M, N, 2 * h, float(alpha), o, kind, st, _s(stream)))
 
 
 def mxfp4_matmul_grouped(a_q, a_s, offsets, b_q, b_s, out, alpha: float = 1.0, d_status=None,
                          stream=None) -> None:
     """out [S, N] = alpha * (rows of group e of A [S, K]) B_e^T, B [E, N, K], groups by
     offsets [E+1]; rows in no group are left as they were."""
-    fn = "mxfp4_matmul_grouped"
-    (S, N), K, E = out.shape, 2 * a_q.shape[-1], offsets.numel() - 1
-    _sizes(fn, _mx_ok(a_q, a_s, (S,), K) and _mx_ok(b_q, b_s, (E, N), K)
-           and _is_i32(offsets))
-    kind = _out_type(fn, out)
-    aq, sa, off, bq, sb, o, st = _ptrs(fn, a_q, a_s, offsets, b_q, b_s, out, d_status)
-    _check(fn, lib.mxfp4_matmul_grouped(aq, sa, off, E, bq, sb, S, N, K, float(alpha), o, kind, st,
+    fn, (u8, i32, _, _) = "mxfp4_matmul_grouped", _dtypes()
+    (S, N), h, kind, E = out.shape, a_q.shape[-1], _out_type(fn, out), offsets.numel() - 1
+    aq, sa, off, bq, sb, o, st = _args(fn, (a_q, (S, h), u8), (a_s, (S, h // 16), u8),
+                                       (offsets, (E + 1,), i32), (b_q, (E, N, h), u8),
+                                       (b_s, (E, N, h // 16), u8), (out, (S, N), (out.dtype,)),
+                                       (d_status, None, i32))
+    _check(fn, lib.mxfp4_matmul_grouped(aq, sa, off, E, bq, sb, S, N, 2 * h, float(alpha), o, kind, st,
                                         _s(stream)))
 
 
@@ -313,13 +297,12 @@ def mxfp4_matmul_grouped_wgrad(a_q, a_s, b_q, b_s, offsets, out, alpha: float = 
                                stream=None) -> None:
     """out [E, M, N] = alpha * A_e B_e^T over the positions of group e of A [M, P] and
     B [N, P] (mxfp4_quantize_transposed_grouped's outputs for the same offsets)."""
-    fn = "mxfp4_matmul_grouped_wgrad"
-    (E, M, N), P = out.shape, 2 * a_q.shape[-1]
-    _sizes(fn, _mx_ok(a_q, a_s, (M,), P) and _mx_ok(b_q, b_s, (N,), P)
-           and offsets.numel() == E + 1 and _is_i32(offsets))
-    kind = _out_type(fn, out)
-    aq, sa, bq, sb, off, o, st = _ptrs(fn, a_q, a_s, b_q, b_s, offsets, out, d_status)
-    _check(fn, lib.mxfp4_matmul_grouped_wgrad(aq, sa, bq, sb, off, E, M, N, P, float(alpha), o, kind,
+    fn, (u8, i32, _, _) = "mxfp4_matmul_grouped_wgrad", _dtypes()
+    (E, M, N), h, kind = out.shape, a_q.shape[-1], _out_type(fn, out)
+    aq, sa, bq, sb, off, o, st = _args(fn, (a_q, (M, h), u8), (a_s, (M, h // 16), u8), (b_q, (N, h), u8),
+                                       (b_s, (N, h // 16), u8), (offsets, (E + 1,), i32),
+                                       (out, (E, M, N), (out.dtype,)), (d_status, None, i32))
+    _check(fn, lib.mxfp4_matmul_grouped_wgrad(aq, sa, bq, sb, off, E, M, N, 2 * h, float(alpha), o, kind,
                                               st, _s(stream)))
 
 
@@ -383,12 +366,13 @@ def moe_combine_backward(dout, y_perm, slot_pos, topk_w, shape: moe_shape, dy_pe
                          dscore=None, stream=None) -> None:
     """Gradients of moe_combine: dy_perm [S][D], dtopk_w [T][k], and dscore [T][k] of the
     k chosen logits through the softmax (the last two when given)."""
-    fn, T, k, D = "moe_combine_backward", shape.T, shape.k, shape.d_model
-    _sizes(fn, _is_bf16(dout) and dout.shape == (T, D) and _is_bf16(dy_perm) and dy_perm.shape == (T * k, D)
-           and _is_i32(slot_pos) and slot_pos.numel() == T * k
-           and (y_perm is None or (_is_bf16(y_perm) and y_perm.shape == (T * k, D)))
-           and all(t is None or (_is_f32(t) and t.shape == (T, k)) for t in (topk_w, dtopk_w, dscore)))
-    g, y, pos, w, dy, dw, ds = _ptrs(fn, dout, y_perm, slot_pos, topk_w, dy_perm, dtopk_w, dscore)
+    fn, (_, i32, f32, b16) = "moe_combine_backward", _dtypes()
+    T, k, D = shape.T, shape.k, shape.d_model
+    rows, per = (T * k, D), (T, k)
+    slots = (T * k,) if slot_pos.ndim == 1 else per
+    g, y, pos, w, dy, dw, ds = _args(fn, (dout, (T, D), b16), (y_perm, rows, b16), (slot_pos, slots, i32),
+                                     (topk_w, per, f32), (dy_perm, rows, b16), (dtopk_w, per, f32),
+                                     (dscore, per, f32))
     _check(fn, lib.moe_combine_backward(g, y, pos, w, shape, dy, dw, ds, _s(stream)))
 
 
@@ -396,13 +380,12 @@ def moe_permute_backward(dx_perm, slot_pos, shape: moe_shape, dx, topk_idx=None,
                          w_router=None, stream=None) -> None:
     """Gradient of moe_permute's gather: dx [T][D], plus the router's share when
     topk_idx [T][k], dscore [T][k] and w_router [E][D] are given."""
-    fn, T, k, D = "moe_permute_backward", shape.T, shape.k, shape.d_model
-    _sizes(fn, _is_bf16(dx_perm) and dx_perm.shape == (T * k, D) and _is_bf16(dx) and dx.shape == (T, D)
-           and _is_i32(slot_pos) and slot_pos.numel() == T * k
-           and (topk_idx is None or (_is_i32(topk_idx) and topk_idx.shape == (T, k)))
-           and (dscore is None or (_is_f32(dscore) and dscore.shape == (T, k)))
-           and (w_router is None or (_is_bf16(w_router) and w_router.shape == (shape.E, D))))
-    g, pos, o, idx, ds, wr = _ptrs(fn, dx_perm, slot_pos, dx, topk_idx, dscore, w_router)
+    fn, (_, i32, f32, b16) = "moe_permute_backward", _dtypes()
+    T, k, D = shape.T, shape.k, shape.d_model
+    slots = (T * k,) if slot_pos.ndim == 1 else (T, k)
+    g, pos, o, idx, ds, wr = _args(fn, (dx_perm, (T * k, D), b16), (slot_pos, slots, i32),
+                                   (dx, (T, D), b16), (topk_idx, (T, k), i32), (dscore, (T, k), f32),
+                                   (w_router, (shape.E, D), b16))
     _check(fn, lib.moe_permute_backward(g, pos, shape, o, idx, ds, wr, _s(stream)))
 
 
