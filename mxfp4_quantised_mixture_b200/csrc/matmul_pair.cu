@@ -3,16 +3,26 @@
 // "MXFP4-based MoE technical review", section 2 (MXFP4 training).  The same
 // products as csrc/matmul.cu, for more than 128 rows of A.
 //
-// What bounds a 4-bit product is not the tensor core but what feeds it: 64 k of
-// a 128 x 224 tile take the tensor core 112 cycles and move 11 KB into and out
-// of shared memory, 196 bytes a cycle where an SM has 128.  A pair of SMs
-// (cta_group::2, M = 256) holds 128 rows of B and half of the A rows in each,
-// so the same 112 cycles per SM move 7.5 KB.
+// What bounds a 4-bit product is not the tensor core but the shared memory that
+// feeds it: 64 k of a 128 x 192 tile take the tensor core 96 cycles and move 10
+// KB into and out of shared memory, 213 bytes a cycle where an SM has 128.  A
+// pair of SMs (cta_group::2, M = 256) holds 128 rows of B and half of the A rows
+// in each, so the same 96 cycles per SM move 7 KB, 146 bytes a cycle; the block
+// scales' way adds a third of that.  Wider tiles would move less per product, but
+// two accumulators of 192 columns and two stages of scales fill tensor memory.
+//   8192 x 5760 x 2880: 86 us alone, 3.2 PFLOP/s (100 us, 2.7 PFLOP/s, in a loop
+//   that draws the power limit); without the scales' loads and the epilogue 63,
+//   without the MMAs too 45, which is 13 TB/s out of L2.  The one-CTA form with
+//   224-row tiles took 139 us.
 //
-// The tensor core takes the block scales from tensor memory.  tcgen05.cp runs
-// in the MMAs' own pipe and cost 240 ns of every stage's 450 (measured on the
-// one-CTA form of this kernel); here four warps write them with tcgen05.st
-// beside the MMAs, two stages deep.
+// The tensor core takes the block scales from tensor memory; here warps write
+// them with tcgen05.st beside the MMAs, two stages deep.  (tcgen05.cp from words
+// laid down in shared memory costs the MMAs nothing, and was measured too: 92-96
+// us, because the words' buffers leave the raw scales too little depth against
+// the copy ring's own queue.)  Waits and issue stay with whole warps and an
+// elected lane: under `lane == 0` four MMAs and one wait took 480 cycles instead
+// of 245.  Arrivals on the other CTA's barriers are at the default scope: with
+// cluster scope each took about a microsecond.
 //
 // Warp roles, in each CTA of the pair:
 //   warp 0       producer: per stage of 512 k its own 128 rows of B and its half
@@ -20,10 +30,9 @@
 //   warp 1       tensor-memory owner; in the first CTA the MMA issuer, in the
 //                second it tells the issuer that a stage's codes have landed
 //   warps 2, 3   scale loaders: cp.async of chunks of 1024 k (32 bytes of a
-//                row, as the three aligned 16-byte pieces that cover them), three
-//                chunks deep.  (Register loads two deep held the products back by
-//                a third: the loads' latency under this kernel's own traffic is
-//                several microseconds.)
+//                row, as the three aligned 16-byte pieces that cover them: rows
+//                start at any byte), three chunks deep; they queue behind the
+//                copy ring's 172 KB
 //   warps 4-11   scale writers, two groups of one per lane quarter: a stage's
 //                bytes shifted into words and put into tensor memory, and the
 //                issuer told

@@ -13,7 +13,9 @@
 // over the lane's own registers, with no shuffle.  The codes (16 bytes per
 // column and block) go through shared memory so that the four blocks of a
 // column leave as one 64-byte run.  HBM-bound: 2 bytes read and 17/32 byte
-// written per element.
+// written per element.  32 matrices of 5760 x 2880: 242 us, 5.6 TB/s, 0.87 of the
+// copy rate; a group of 32768 x 2880 rows 57 us.  (256 rows to a CTA were 10%
+// slower; 64-bit divisions in the tile arithmetic cost 30%.)
 //
 // Grouped rows (a ragged batch sorted by expert): the output positions of a
 // group start at a multiple of 128 and are zero behind its last row, so a
