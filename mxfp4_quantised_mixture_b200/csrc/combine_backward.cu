@@ -66,10 +66,10 @@ __global__ void __launch_bounds__(kThreads)
           acc[j] = fmaf(gf[2 * q + 1], __uint_as_float(yw[q] & 0xFFFF0000u), acc[j]);
         }
         uint4 o;
-        o.x = pack_bf16x2(wt[j] * gf[0], wt[j] * gf[1]);
-        o.y = pack_bf16x2(wt[j] * gf[2], wt[j] * gf[3]);
-        o.z = pack_bf16x2(wt[j] * gf[4], wt[j] * gf[5]);
-        o.w = pack_bf16x2(wt[j] * gf[6], wt[j] * gf[7]);
+        o.x = cvt_bf16x2(wt[j] * gf[0], wt[j] * gf[1]);
+        o.y = cvt_bf16x2(wt[j] * gf[2], wt[j] * gf[3]);
+        o.z = cvt_bf16x2(wt[j] * gf[4], wt[j] * gf[5]);
+        o.w = cvt_bf16x2(wt[j] * gf[6], wt[j] * gf[7]);
         dy[row[j] + v] = o;
       }
     }

@@ -67,13 +67,6 @@ __device__ __forceinline__ Groups group_table(void* at) {
   return g;
 }
 
-// two fp32 -> bf16x2, round to nearest even (lo in the low half)
-__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 __device__ __forceinline__ void abort_cta(volatile int* abort, int32_t* status) {
   *abort = 1;
   record_status(status, MOE_ERR_TIMEOUT);

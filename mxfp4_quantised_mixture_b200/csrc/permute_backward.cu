@@ -63,10 +63,10 @@ __global__ void __launch_bounds__(kThreads)
       for (int j = 0; j < K; ++j) add8(acc, wr[j], ds[j]);
     }
     uint4 o;
-    o.x = pack_bf16x2(acc[0], acc[1]);
-    o.y = pack_bf16x2(acc[2], acc[3]);
-    o.z = pack_bf16x2(acc[4], acc[5]);
-    o.w = pack_bf16x2(acc[6], acc[7]);
+    o.x = cvt_bf16x2(acc[0], acc[1]);
+    o.y = cvt_bf16x2(acc[2], acc[3]);
+    o.z = cvt_bf16x2(acc[4], acc[5]);
+    o.w = cvt_bf16x2(acc[6], acc[7]);
     dx[i] = o;
   }
 }
