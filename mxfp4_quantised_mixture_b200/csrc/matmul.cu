@@ -94,7 +94,7 @@ __device__ __forceinline__ void stage_columns(uint32_t acc, const Work& w, float
   }
 }
 
-template <int NT>
+template <int NT, int OUT>
 __global__ void __launch_bounds__(threads(NT), ctas_per_sm(NT))
     mxfp4_matmul_kernel(const __grid_constant__ CUtensorMap map_x,
                         const __grid_constant__ CUtensorMap map_y, const Args a) {
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(threads(NT), ctas_per_sm(NT))
       const int half = kEpi == 8 ? (all / 2 + 31) & ~31 : all;
       const int c0 = part ? min(half, all) : 0, c1 = part ? all : min(half, all);
       if (split == 1)
-        store_columns(acc, a, w, n, c0, c1);
+        store_columns<OUT>(acc, a, w, n, c0, c1);
       else
         stage_columns(acc, w, reinterpret_cast<float*>(smem), q * 32 + lane, c0, c1);
       tc::tc_fence_before();
@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(threads(NT), ctas_per_sm(NT))
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           if (n + k >= a.x_rows) break;
-          if (a.out_f32)
+          if (OUT == kFp32)
             static_cast<float*>(a.out)[at + k] = a.alpha * v[k];
           else
             static_cast<uint16_t*>(a.out)[at + k] = static_cast<uint16_t>(cvt_bf16x2(a.alpha * v[k], 0.f));
@@ -392,14 +392,14 @@ struct ClusterLaunch {
 };
 
 // How many clusters of `size` CTAs the device runs at a time (asked once).
-template <int NT>
+template <int NT, int OUT>
 int clusters_at_once(int dev, int size) {
   static std::atomic<int> known[64][9];
   const bool keep = dev >= 0 && dev < 64;
   int n = keep ? known[dev][size].load() - 1 : -1;
   if (n >= 0) return n;
   ClusterLaunch l(static_cast<unsigned>(size), threads(NT), smem_bytes(NT), size, nullptr);
-  if (cudaOccupancyMaxActiveClusters(&n, mxfp4_matmul_kernel<NT>, &l.cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&n, mxfp4_matmul_kernel<NT, OUT>, &l.cfg) != cudaSuccess) {
     cudaGetLastError();
     return 0;
   }
@@ -407,8 +407,8 @@ int clusters_at_once(int dev, int size) {
   return n;
 }
 
-template <int NT>
-moe_status launch_nt(Args a, const uint8_t* xq, const uint8_t* yq, cudaStream_t stream) {
+template <int NT, int OUT>
+moe_status launch_one(Args a, const uint8_t* xq, const uint8_t* yq, cudaStream_t stream) {
   const int64_t max_work = plan_tiles(&a, BX, NT);
   if (max_work > kMaxTiles) return MOE_ERR_SHAPE;
   static std::atomic<uint64_t> done{0};
@@ -419,7 +419,7 @@ moe_status launch_nt(Args a, const uint8_t* xq, const uint8_t* yq, cudaStream_t 
   }
   const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
   if (!bit || !(done.load() & bit)) {
-    if (cudaFuncSetAttribute(mxfp4_matmul_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(mxfp4_matmul_kernel<NT, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              smem_bytes(NT)) != cudaSuccess) {
       cudaGetLastError();
       return MOE_ERR_CUDA;
@@ -437,17 +437,26 @@ moe_status launch_nt(Args a, const uint8_t* xq, const uint8_t* yq, cudaStream_t 
   int64_t split = sms / max_work;
   if (split > nst / 2) split = nst / 2;
   if (split > 8) split = 8;
-  while (split > 1 && clusters_at_once<NT>(dev, static_cast<int>(split)) < max_work) --split;
+  while (split > 1 && clusters_at_once<NT, OUT>(dev, static_cast<int>(split)) < max_work) --split;
   a.split = split < 2 ? 1 : static_cast<int>(split);
   const int64_t cap = sms * ctas_per_sm(NT);
   const int64_t ctas = a.split > 1 ? max_work * a.split : (max_work < cap ? max_work : cap);
   ClusterLaunch l(static_cast<unsigned>(ctas), threads(NT), smem_bytes(NT), a.split, stream);
   const cudaLaunchConfig_t& cfg = l.cfg;
-  if (cudaLaunchKernelEx(&cfg, mxfp4_matmul_kernel<NT>, mx, my, a) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, mxfp4_matmul_kernel<NT, OUT>, mx, my, a) != cudaSuccess) {
     cudaGetLastError();
     return MOE_ERR_CUDA;
   }
   return MOE_OK;
+}
+
+template <int NT>
+moe_status launch_nt(const Args& a, int out_type, const uint8_t* xq, const uint8_t* yq, cudaStream_t stream) {
+  switch (out_of(out_type, a.x_rows)) {
+    case kFp32: return launch_one<NT, kFp32>(a, xq, yq, stream);
+    case kBf16Pairs: return launch_one<NT, kBf16Pairs>(a, xq, yq, stream);
+    default: return launch_one<NT, kBf16>(a, xq, yq, stream);
+  }
 }
 
 // Rows of A per tile: `rows` is what one tile may meet, twice the mean of a
@@ -459,16 +468,17 @@ moe_status launch_nt(Args a, const uint8_t* xq, const uint8_t* yq, cudaStream_t 
 // that three CTAs and more can share each one's k: 300 x 300 x 16384 then takes 13
 // us instead of 26, 1000 x 600 x 8192 15 instead of 18, while 512 x 2880 x 8192,
 // at 92 tiles, takes 21 instead of 18.5.
-moe_status run(Args a, const uint8_t* xq, const uint8_t* yq, int64_t rows, cudaStream_t stream) {
+moe_status run(const Args& a, int out_type, const uint8_t* xq, const uint8_t* yq, int64_t rows,
+               cudaStream_t stream) {
   if (rows > 128 && a.x_rows > 128) {
     Args few = a;
-    if (3 * plan_tiles(&few, BX, 128) > sm_count()) return launch_pair(a, xq, yq, stream);
+    if (3 * plan_tiles(&few, BX, 128) > sm_count()) return launch_pair(a, out_type, xq, yq, stream);
   }
   const int NT = rows <= 32 ? 32 : (rows <= 64 ? 64 : 128);
   switch (NT) {
-    case 32: return launch_nt<32>(a, xq, yq, stream);
-    case 64: return launch_nt<64>(a, xq, yq, stream);
-    default: return launch_nt<128>(a, xq, yq, stream);
+    case 32: return launch_nt<32>(a, out_type, xq, yq, stream);
+    case 64: return launch_nt<64>(a, out_type, xq, yq, stream);
+    default: return launch_nt<128>(a, out_type, xq, yq, stream);
   }
 }
 
@@ -509,9 +519,8 @@ moe_status mxfp4_matmul(const uint8_t* a_q, const uint8_t* a_s, const uint8_t* b
   a.K = K;
   a.alpha = alpha;
   a.out = out;
-  a.out_f32 = out_type == MOE_OUT_FP32;
   a.status = d_status;
-  return run(a, b_q, a_q, M, static_cast<cudaStream_t>(stream));
+  return run(a, out_type, b_q, a_q, M, static_cast<cudaStream_t>(stream));
 }
 
 moe_status mxfp4_matmul_grouped(const uint8_t* a_q, const uint8_t* a_s, const int32_t* offsets,
@@ -540,9 +549,8 @@ moe_status mxfp4_matmul_grouped(const uint8_t* a_q, const uint8_t* a_s, const in
   a.S = S;
   a.alpha = alpha;
   a.out = out;
-  a.out_f32 = out_type == MOE_OUT_FP32;
   a.status = d_status;
-  return run(a, b_q, a_q, 2 * ((S + E - 1) / E), static_cast<cudaStream_t>(stream));
+  return run(a, out_type, b_q, a_q, 2 * ((S + E - 1) / E), static_cast<cudaStream_t>(stream));
 }
 
 moe_status mxfp4_matmul_grouped_wgrad(const uint8_t* a_q, const uint8_t* a_s, const uint8_t* b_q,
@@ -583,9 +591,8 @@ moe_status mxfp4_matmul_grouped_wgrad(const uint8_t* a_q, const uint8_t* a_s, co
   a.S = P;  // a group never has more rows than positions
   a.alpha = alpha;
   a.out = out;
-  a.out_f32 = out_type == MOE_OUT_FP32;
   a.status = d_status;
-  return run(a, b_q, a_q, M, static_cast<cudaStream_t>(stream));
+  return run(a, out_type, b_q, a_q, M, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

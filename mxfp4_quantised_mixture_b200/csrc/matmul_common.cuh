@@ -26,6 +26,11 @@ constexpr int64_t kMaxTiles = (int64_t(1) << 31) - (1 << 16);  // tile numbers, 
 
 enum Mode : int { kDense = 0, kGrouped = 1, kWgrad = 2 };
 
+// How the output is stored, a template argument of the kernels: with all three
+// ways in one kernel the epilogue's instruction fetches took a fifth of the
+// weight gradient's time (328 against 274 us in fp32, 297 against 228 in bf16).
+enum Out : int { kFp32 = 0, kBf16Pairs = 1, kBf16 = 2 };  // pairs: rows of even length
+
 struct Args {
   int mode, E;
   FastDiv xt, yt;          // tiles along B's rows, and along A's
@@ -40,7 +45,6 @@ struct Args {
   int64_t S;               // bound of the offsets' values
   float alpha;
   void* out;
-  int out_f32;
   int32_t* status;
 };
 
@@ -236,46 +240,37 @@ __device__ __forceinline__ void store16_pairs(const uint32_t (&r)[16], float alp
 
 // Columns [c0, c1) of a tile's accumulator (a multiple of 16 of them, the last
 // ones possibly past its ny rows), to output column n.
+template <int OUT>
 __device__ __forceinline__ void store_columns(uint32_t acc, const Args& a, const Work& w, int64_t n,
                                               int c0, int c1) {
+  constexpr int kSize = OUT == kFp32 ? 4 : 2;
   const bool live = n < a.x_rows;
   const uint32_t ld = static_cast<uint32_t>(a.x_rows);
-  const bool pairs = !a.out_f32 && (ld & 1) == 0;
-  const int size = a.out_f32 ? 4 : 2;
-  char* p = static_cast<char*>(a.out) + ((w.out_row + c0) * a.x_rows + n) * size;
-  if (pairs && (threadIdx.x & 1)) p += static_cast<int64_t>(ld) * 2 - 2;
-  const int64_t step = static_cast<int64_t>(16) * ld * size;
-  uint32_t r[2][16];
+  char* p = static_cast<char*>(a.out) + ((w.out_row + c0) * a.x_rows + n) * kSize;
+  if (OUT == kBf16Pairs && (threadIdx.x & 1)) p += static_cast<int64_t>(ld) * 2 - 2;
+  const int64_t step = static_cast<int64_t>(16) * ld * kSize;
+  uint32_t r[16];
 #pragma unroll
-  for (int k = 0; k < 16; ++k) r[0][k] = r[1][k] = 0u;  // an empty sum, if nothing is loaded
-  const auto put = [&](const uint32_t (&v)[16], int ny) {
-    if (pairs) {  // lanes 2j, 2j + 1 exist together
-      if (!live) ny = 0;
-      if (__all_sync(0xFFFFFFFFu, ny >= 16))
-        store16_pairs<true>(v, a.alpha, p, 2 * ld, ny);
-      else
-        store16_pairs<false>(v, a.alpha, p, 2 * ld, ny);
-    } else if (live) {
-      if (a.out_f32) {
-        if (ny >= 16)
-          store16<true, true>(v, a.alpha, p, ld, ny);
-        else
-          store16<true, false>(v, a.alpha, p, ld, ny);
-      } else {
-        store16<false, false>(v, a.alpha, p, ld, ny);
-      }
-    }
-    p += step;
-  };
-  for (int c = c0; c < c1; c += 32) {
-    const bool two = c + 16 < c1;
+  for (int k = 0; k < 16; ++k) r[k] = 0u;  // an empty sum, if nothing is loaded
+#pragma unroll 1
+  for (int c = c0; c < c1; c += 16) {
     if (w.steps > 0) {
-      tc::tmem_ld16(acc + c, r[0]);
-      if (two) tc::tmem_ld16(acc + c + 16, r[1]);
+      tc::tmem_ld16(acc + c, r);
       tc::tmem_ld_wait();
     }
-    put(r[0], w.ny - c);
-    if (two) put(r[1], w.ny - c - 16);
+    const int ny = live ? w.ny - c : 0;
+    if (__all_sync(0xFFFFFFFFu, ny >= 16)) {
+      if (OUT == kBf16Pairs)  // lanes 2j, 2j + 1 exist together
+        store16_pairs<true>(r, a.alpha, p, 2 * ld, ny);
+      else
+        store16<OUT == kFp32, true>(r, a.alpha, p, ld, ny);
+    } else {
+      if (OUT == kBf16Pairs)
+        store16_pairs<false>(r, a.alpha, p, 2 * ld, ny);
+      else
+        store16<OUT == kFp32, false>(r, a.alpha, p, ld, ny);
+    }
+    p += step;
   }
 }
 
@@ -388,8 +383,14 @@ inline bool encode_codes(CUtensorMap* map, const void* base, int64_t row, int64_
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The way to store rows of x_rows elements of a type.
+inline Out out_of(int out_type, int64_t x_rows) {
+  return out_type == MOE_OUT_FP32 ? kFp32 : (x_rows % 2 == 0 ? kBf16Pairs : kBf16);
+}
+
 // The two-CTA kernel (csrc/matmul_pair.cu).
-moe_status launch_pair(Args a, const uint8_t* xq, const uint8_t* yq, cudaStream_t stream);
+moe_status launch_pair(const Args& a, int out_type, const uint8_t* xq, const uint8_t* yq,
+                       cudaStream_t stream);
 
 }  // namespace mm
 }  // namespace moe

@@ -92,6 +92,7 @@ __device__ __forceinline__ bool lead_wait(uint64_t* bar, uint32_t parity, volati
   return r;
 }
 
+template <int OUT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mxfp4_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_x,
                              const __grid_constant__ CUtensorMap map_y, const Args a) {
@@ -410,7 +411,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int all = (w.ny + 15) & ~15, half = (all / 2 + 31) & ~31;
       const int part = (warp - kEpi0) >> 2;
       const int c0 = part ? min(half, all) : 0, c1 = part ? all : min(half, all);
-      store_columns(acc, a, w, n, c0, c1);
+      store_columns<OUT>(acc, a, w, n, c0, c1);
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive_cluster(tc::cluster_addr(&dempty[b], 0));
@@ -430,11 +431,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
-}  // namespace
-
-namespace mm {
-
-moe_status launch_pair(Args a, const uint8_t* xq, const uint8_t* yq, cudaStream_t stream) {
+template <int OUT>
+moe_status launch_one(Args a, const uint8_t* xq, const uint8_t* yq, cudaStream_t stream) {
   const int64_t most = plan_tiles(&a, BX, NT);
   if (most > kMaxTiles) return MOE_ERR_SHAPE;
   static std::atomic<uint64_t> done{0};
@@ -445,7 +443,7 @@ moe_status launch_pair(Args a, const uint8_t* xq, const uint8_t* yq, cudaStream_
   }
   const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
   if (!bit || !(done.load() & bit)) {
-    if (cudaFuncSetAttribute(mxfp4_matmul_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(mxfp4_matmul_pair_kernel<OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kSmem) != cudaSuccess) {
       cudaGetLastError();
       return MOE_ERR_CUDA;
@@ -458,7 +456,20 @@ moe_status launch_pair(Args a, const uint8_t* xq, const uint8_t* yq, cudaStream_
     return MOE_ERR_CUDA;
   const int64_t pairs = sm_count() / 2;
   const dim3 grid(static_cast<unsigned>(2 * (most < pairs ? most : pairs)));
-  return launch(mxfp4_matmul_pair_kernel, grid, dim3(kThreads), kSmem, stream, mx, my, a);
+  return launch(mxfp4_matmul_pair_kernel<OUT>, grid, dim3(kThreads), kSmem, stream, mx, my, a);
+}
+
+}  // namespace
+
+namespace mm {
+
+moe_status launch_pair(const Args& a, int out_type, const uint8_t* xq, const uint8_t* yq,
+                       cudaStream_t stream) {
+  switch (out_of(out_type, a.x_rows)) {
+    case kFp32: return launch_one<kFp32>(a, xq, yq, stream);
+    case kBf16Pairs: return launch_one<kBf16Pairs>(a, xq, yq, stream);
+    default: return launch_one<kBf16>(a, xq, yq, stream);
+  }
 }
 
 }  // namespace mm
