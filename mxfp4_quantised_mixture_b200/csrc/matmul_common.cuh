@@ -28,7 +28,8 @@ enum Mode : int { kDense = 0, kGrouped = 1, kWgrad = 2 };
 
 // How the output is stored, a template argument of the kernels: with all three
 // ways in one kernel the epilogue's instruction fetches took a fifth of the
-// weight gradient's time (328 against 274 us in fp32, 297 against 228 in bf16).
+// weight gradient's time (32 experts of 2880 x 2880, 32768
+// rows: 328 against 273 us in fp32, 297 against 231 in bf16).
 enum Out : int { kFp32 = 0, kBf16Pairs = 1, kBf16 = 2 };  // pairs: rows of even length
 
 struct Args {

@@ -10,7 +10,7 @@
 // in each, so the same 96 cycles per SM move 7 KB, 146 bytes a cycle; the block
 // scales' way adds a third of that.  Wider tiles would move less per product, but
 // two accumulators of 192 columns and two stages of scales fill tensor memory.
-//   8192 x 5760 x 2880: 86 us alone, 3.2 PFLOP/s (100 us, 2.7 PFLOP/s, in a loop
+//   8192 x 5760 x 2880: 85 us alone, 3.2 PFLOP/s (96 us, 2.8 PFLOP/s, in a loop
 //   that draws the power limit); without the scales' loads and the epilogue 63,
 //   without the MMAs too 45, which is 13 TB/s out of L2.  The one-CTA form with
 //   224-row tiles took 139 us.
