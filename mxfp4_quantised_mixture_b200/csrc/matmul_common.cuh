@@ -78,10 +78,11 @@ __device__ __forceinline__ void abort_cta(volatile int* abort, int32_t* status) 
 }
 
 // Every lane of a converged warp waits for a phase; the answer is the same in
-// all of them.
+// all of them.  CLUSTER: the other CTA arrives at the barrier too.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool all_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
                                          int32_t* status) {
-  if (__all_sync(0xFFFFFFFFu, tc::mbar_wait(bar, parity, abort, kWaitLimitNs))) return true;
+  if (__all_sync(0xFFFFFFFFu, tc::mbar_wait<CLUSTER>(bar, parity, abort, kWaitLimitNs))) return true;
   abort_cta(abort, status);
   return false;
 }

@@ -21,8 +21,11 @@
 // us, because the words' buffers leave the raw scales too little depth against
 // the copy ring's own queue.)  Waits and issue stay with whole warps and an
 // elected lane: under `lane == 0` four MMAs and one wait took 480 cycles instead
-// of 245.  Arrivals on the other CTA's barriers are at the default scope: with
-// cluster scope each took about a microsecond.
+// of 245.  Arrivals on the other CTA's barriers release this CTA's shared memory
+// at cluster scope by a fence for it alone: as mbarrier.arrive.release.cluster
+// they cost a fifth of the time (dense 8192 x 5760 x 2880 in a loop: the second
+// CTA's copies alone by that form 93 us, the scale writers' arrivals too 114,
+// against 81 by the fence).
 //
 // Warp roles, in each CTA of the pair:
 //   warp 0       producer: per stage of 512 k its own 128 rows of B and its half
@@ -195,12 +198,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t idesc = tc::idesc_mxf4(BX, (w.ny + STEP - 1) & ~(STEP - 1));
         const uint32_t d = tmem + (it & 1) * NT;
         // accumulator it & 1 was last used by tile it - 2
-        if (it >= 2 && !all_wait(&dempty[it & 1], ((it >> 1) - 1) & 1, abort_flag, a.status)) break;
+        if (it >= 2 && !all_wait<true>(&dempty[it & 1], ((it >> 1) - 1) & 1, abort_flag, a.status)) break;
         const int nst = pair_stages(w);
         for (int st = 0; st < nst; ++st) {
           // its own codes, then the other CTA's and both CTAs' scales
           if (!all_wait(&full[s], phase, abort_flag, a.status) ||
-              !all_wait(&ready[s], phase, abort_flag, a.status)) {
+              !all_wait<true>(&ready[s], phase, abort_flag, a.status)) {
             ok = false;
             break;
           }
@@ -244,7 +247,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
     } else {
-      // the second CTA: its codes' arrival, passed on to the issuer
+      // the second CTA: its codes' arrival, passed on to the issuer, whose MMAs
+      // read them (the tcgen05 fences order tensor memory only)
       const uint32_t to = tc::cluster_addr(ready, 0);
       uint32_t s = 0, phase = 0;
       bool ok = true;

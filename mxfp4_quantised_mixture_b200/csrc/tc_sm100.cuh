@@ -58,6 +58,22 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+// The same for a barrier at which other CTAs of the cluster arrive (with
+// mbar_arrive_cluster): a completed phase acquires the shared memory that they
+// pass on.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  if (ok != 0) asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
+  return ok != 0;
+}
+
 __device__ __forceinline__ uint64_t globaltimer_ns() {
   uint64_t t;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
@@ -67,12 +83,15 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
 // Wait for the phase with the given parity to complete.  Gives up after
 // `limit_ns` of wall time (or when *abort becomes non-zero) and returns false;
 // the caller then records a timeout and unwinds.
+// CLUSTER: other CTAs of the cluster arrive at the barrier.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const volatile int* abort,
                                           uint64_t limit_ns) {
-  if (mbar_try_wait(bar, parity)) return true;
+  const auto done = [&] { return CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
+  if (done()) return true;
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (done()) return true;
     if ((i & 63u) == 0) {
       if (*abort) return false;
       if (globaltimer_ns() - t0 > limit_ns) return false;
@@ -168,13 +187,17 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   return v;
 }
 
-// Arrive on a barrier of the cluster (a shared::cluster address).  At the
-// default scope: it passes on no global memory, only tensor memory (ordered by
-// the tcgen05 fences around it) and copies its thread has seen complete.  With
-// cluster scope the arrival waits for every earlier memory operation of the
-// thread, about a microsecond.
+// Arrive on a barrier of another CTA of the cluster (a shared::cluster address),
+// passing on the shared memory of this CTA as its thread has seen it, completed
+// copies among it, to a wait that acquires with mbar_try_wait_cluster.  The fence
+// orders shared memory alone: mbarrier.arrive.release.cluster would order every
+// earlier memory operation of the thread, which takes about a microsecond where
+// loads or stores are in flight.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_addr) : "memory");
+  asm volatile(
+      "fence.release.sync_restrict::shared::cta.cluster;\n\t"
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_addr)
+      : "memory");
 }
 
 __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
