@@ -344,6 +344,7 @@ MOE_API int64_t mxfp4_transposed_width(int64_t rows, int32_t E);
  *   w_bf16   in   [batch][rows][cols] bf16
  *   batch    in   >= 0;  rows in >= 0 (either 0: a no-op), rows <= 2^31
  *   cols     in   multiple of 8 in [8, 2^31];  batch*rows*cols <= 2^40
+ *                 and batch * ceil(P/128) * ceil(cols/128) <= 2^31
  *   q_packed out  [batch][cols][P/2], P = mxfp4_transposed_width(rows, 0)
  *   scales   out  [batch][cols][P/32]
  *   d_status out  nullable; MOE_ERR_NONFINITE if a block holds NaN or Inf
@@ -360,7 +361,7 @@ MOE_API moe_status mxfp4_quantize_transposed(const uint16_t* w_bf16, int64_t bat
  * of 128 positions meets two groups.  A group's positions from its last row to
  * the next multiple of 128 are zero; positions behind the last group are left
  * as they were (mxfp4_matmul_grouped_wgrad reads none of them).
- *   w_bf16   in   [rows][cols] bf16, cols a multiple of 8
+ *   w_bf16   in   [rows][cols] bf16, rows and cols as above with batch = 1
  *   offsets  in   [E+1] device, ascending, in [0, rows], 1 <= E <= 256; rows in
  *                 no group are not read
  *   q_packed out  [cols][P/2], P = mxfp4_transposed_width(rows, E)

@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// Checks shared by both entries; `need_offsets` for the grouped one.
+// Checks of the pointers shared by both entries; n: rows of the input.
 moe_status check(const uint16_t* w, int64_t n, const uint8_t* q, const uint8_t* s,
                  const int32_t* d_status) {
   if (n > 0 && (!w || !q || !s)) return MOE_ERR_INVALID_ARG;
@@ -143,7 +143,6 @@ moe_status launch_tiles(const uint16_t* w, int64_t batch, int64_t rows, int64_t 
                         int32_t E, int64_t P, uint8_t* q, uint8_t* s, int32_t* d_status, moe_stream stream) {
   const int64_t ct = (cols + kCols - 1) / kCols, rt = (P + kRows - 1) / kRows;
   const int64_t cap = static_cast<int64_t>(sm_count()) * 8;
-  if (batch * rt >= (int64_t(1) << 31) / ct - cap) return MOE_ERR_SHAPE;
   const int64_t tiles = batch * rt * ct;
   return launch(quantize_transposed_kernel<GROUPED>, dim3(static_cast<unsigned>(tiles < cap ? tiles : cap)),
                 dim3(kThreads), 0, static_cast<cudaStream_t>(stream), reinterpret_cast<const uint32_t*>(w),
@@ -157,6 +156,13 @@ bool sizes_ok(int64_t batch, int64_t rows, int64_t cols) {
   if (rows > (int64_t(1) << 31) || cols > (int64_t(1) << 31) || batch > lim) return false;
   if (rows > 0 && (cols > lim / rows || (batch > 0 && batch > lim / (rows * cols)))) return false;
   return true;
+}
+
+// A tile's number fits the division by multiplication (below 2^31).  A tile writes
+// 8 columns of 16 bytes and more, so a refused output would not fit in 256 GB.
+bool tiles_ok(int64_t batch, int64_t cols, int64_t P) {
+  const int64_t ct = (cols + kCols - 1) / kCols, rt = (P + kRows - 1) / kRows;
+  return batch * rt <= (int64_t(1) << 31) / ct;
 }
 
 }  // namespace
@@ -177,11 +183,12 @@ moe_status mxfp4_quantize_transposed(const uint16_t* w_bf16, int64_t batch, int6
   using namespace moe;
   if (!sizes_ok(batch, rows, cols)) return MOE_ERR_SHAPE;
   if (batch == 0 || rows == 0) return MOE_OK;
+  const int64_t P = mxfp4_transposed_width(rows, 0);
+  if (!tiles_ok(batch, cols, P)) return MOE_ERR_SHAPE;
   moe_status st = check(w_bf16, batch * rows, q_packed, scales, d_status);
   if (st != MOE_OK) return st;
   if ((st = check_device()) != MOE_OK) return st;
-  return launch_tiles<false>(w_bf16, batch, rows, cols, nullptr, 0, mxfp4_transposed_width(rows, 0),
-                             q_packed, scales, d_status, stream);
+  return launch_tiles<false>(w_bf16, batch, rows, cols, nullptr, 0, P, q_packed, scales, d_status, stream);
 }
 
 moe_status mxfp4_quantize_transposed_grouped(const uint16_t* w_bf16, int64_t rows, int64_t cols,
@@ -192,6 +199,7 @@ moe_status mxfp4_quantize_transposed_grouped(const uint16_t* w_bf16, int64_t row
   if (!sizes_ok(1, rows, cols) || E < 1 || E > kMaxGroups) return MOE_ERR_SHAPE;
   if (rows == 0) return MOE_OK;
   const int64_t P = mxfp4_transposed_width(rows, E);
+  if (!tiles_ok(1, cols, P)) return MOE_ERR_SHAPE;
   if (!offsets || !aligned16(offsets)) return MOE_ERR_INVALID_ARG;
   moe_status st = check(w_bf16, rows, q_packed, scales, d_status);
   if (st != MOE_OK) return st;
