@@ -388,13 +388,27 @@ MOE_API moe_status mxfp4_quantize_transposed_grouped(const uint16_t* w_bf16, int
  *   a_q, a_s in   MXFP4 [M][K];  b_q, b_s in MXFP4 [N][K]
  *   M, N     in   [0, 2^27] (0: a no-op);  K a multiple of 32 in [32, 2^24]
  *   out      out  [M][N], out_type MOE_OUT_BF16 or MOE_OUT_FP32
- *   d_status out  nullable; MOE_ERR_TIMEOUT if a bounded wait gave up (never
- *                 written otherwise)
+ *   d_status out  nullable; MOE_ERR_TIMEOUT if a bounded wait gave up, and
+ *                 `out` is then unspecified (never written otherwise)
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_SHAPE, MOE_ERR_UNSUPPORTED,
  * MOE_ERR_CUDA.                                                          */
 MOE_API moe_status mxfp4_matmul(const uint8_t* a_q, const uint8_t* a_s, const uint8_t* b_q,
                                 const uint8_t* b_s, int64_t M, int64_t N, int64_t K, float alpha,
                                 void* out, int32_t out_type, int32_t* d_status, moe_stream stream);
+
+/* mxfp4_matmul_ex -- mxfp4_matmul with testing support.
+ *   test_timeout_cta  -1 in normal use.  A value c >= 0 makes the first wait
+ *         of the MMA warp in CTA c give up after a short bounded wait on a
+ *         barrier that nothing completes, as a real timeout would: the device
+ *         status word becomes MOE_ERR_TIMEOUT, the CTA unwinds after draining
+ *         its own copies and MMAs (where CTAs work in pairs, the other one
+ *         gives up after the wait limit, 2 s), and `out` is unspecified.  The
+ *         next call runs normally.  The grouped products run the same kernels.
+ * Otherwise the same operation, passages, arguments and errors.          */
+MOE_API moe_status mxfp4_matmul_ex(const uint8_t* a_q, const uint8_t* a_s, const uint8_t* b_q,
+                                   const uint8_t* b_s, int64_t M, int64_t N, int64_t K,
+                                   float alpha, void* out, int32_t out_type, int32_t* d_status,
+                                   int32_t test_timeout_cta, moe_stream stream);
 
 /* mxfp4_matmul_grouped -- the product of every expert's rows with its matrix.
  * For every row r in [offsets[e], offsets[e+1]):

@@ -92,6 +92,8 @@ def _load() -> ctypes.CDLL:
     lib.mxfp4_quantize_transposed_grouped.restype = st
     lib.mxfp4_matmul.argtypes = [vp, vp, vp, vp, i64, i64, i64, f32, vp, i32, vp, vp]
     lib.mxfp4_matmul.restype = st
+    lib.mxfp4_matmul_ex.argtypes = [vp, vp, vp, vp, i64, i64, i64, f32, vp, i32, vp, i32, vp]
+    lib.mxfp4_matmul_ex.restype = st
     lib.mxfp4_matmul_grouped.argtypes = [vp, vp, vp, i32, vp, vp, i64, i64, i64, f32, vp, i32, vp,
                                          vp]
     lib.mxfp4_matmul_grouped.restype = st
@@ -269,14 +271,28 @@ def mxfp4_quantize_transposed_grouped(w_bf16, offsets, q_packed, scales, d_statu
     _check(fn, lib.mxfp4_quantize_transposed_grouped(w, S, C, off, E, q, sc, st, _s(stream)))
 
 
-def mxfp4_matmul(a_q, a_s, b_q, b_s, out, alpha: float = 1.0, d_status=None, stream=None) -> None:
-    """out [M, N] (bf16 or fp32) = alpha * A B^T of MXFP4 A [M, K] and B [N, K]."""
-    fn, (u8, i32, _, _) = "mxfp4_matmul", _dtypes()
+def _matmul_args(fn: str, a_q, a_s, b_q, b_s, out, alpha: float, d_status) -> tuple:
+    u8, i32, _, _ = _dtypes()
     (M, N), h, kind = out.shape, a_q.shape[-1], _out_type(fn, out)
     aq, sa, bq, sb, o, st = _args(fn, (a_q, (M, h), u8), (a_s, (M, h // 16), u8), (b_q, (N, h), u8),
                                   (b_s, (N, h // 16), u8), (out, (M, N), (out.dtype,)),
                                   (d_status, None, i32))
-    _check(fn, lib.mxfp4_matmul(aq, sa, bq, sb, M, N, 2 * h, float(alpha), o, kind, st, _s(stream)))
+    return aq, sa, bq, sb, M, N, 2 * h, float(alpha), o, kind, st
+
+
+def mxfp4_matmul(a_q, a_s, b_q, b_s, out, alpha: float = 1.0, d_status=None, stream=None) -> None:
+    """out [M, N] (bf16 or fp32) = alpha * A B^T of MXFP4 A [M, K] and B [N, K]."""
+    fn = "mxfp4_matmul"
+    args = _matmul_args(fn, a_q, a_s, b_q, b_s, out, alpha, d_status)
+    _check(fn, lib.mxfp4_matmul(*args, _s(stream)))
+
+
+def mxfp4_matmul_ex(a_q, a_s, b_q, b_s, out, alpha: float = 1.0, d_status=None,
+                    test_timeout_cta: int = -1, stream=None) -> None:
+    """mxfp4_matmul; test_timeout_cta >= 0 is testing support (see the C header)."""
+    fn = "mxfp4_matmul_ex"
+    args = _matmul_args(fn, a_q, a_s, b_q, b_s, out, alpha, d_status)
+    _check(fn, lib.mxfp4_matmul_ex(*args, int(test_timeout_cta), _s(stream)))
 
 
 def mxfp4_matmul_grouped(a_q, a_s, offsets, b_q, b_s, out, alpha: float = 1.0, d_status=None,
@@ -425,8 +441,8 @@ def alloc_workspace(shape: moe_shape, which: int, device="cuda"):
 __all__ = ["moe_shape", "make_shape", "MoeError", "mxfp4_quantize", "mxfp4_quantize_sr_rht",
            "MOE_QUANT_RHT", "MOE_QUANT_SR",
            "mxfp4_transposed_width", "mxfp4_quantize_transposed",
-           "mxfp4_quantize_transposed_grouped", "mxfp4_matmul", "mxfp4_matmul_grouped",
-           "mxfp4_matmul_grouped_wgrad", "MOE_OUT_BF16", "MOE_OUT_FP32",
+           "mxfp4_quantize_transposed_grouped", "mxfp4_matmul", "mxfp4_matmul_ex",
+           "mxfp4_matmul_grouped", "mxfp4_matmul_grouped_wgrad", "MOE_OUT_BF16", "MOE_OUT_FP32",
            "moe_combine_backward", "moe_permute_backward", "moe_route",
            "moe_router_topk", "moe_permute",
            "moe_expert_mlp", "moe_expert_mlp_ex", "moe_expert_mlp_unquantised", "moe_combine", "moe_layer_forward",

@@ -113,7 +113,8 @@ __global__ void __launch_bounds__(threads(NT), ctas_per_sm(NT))
   uint64_t* dfull = sempty + kChunkSlots;  // [2] accumulator complete
   uint64_t* dempty = dfull + 2;            // [2] accumulator read
   uint64_t* drain = dempty + 2;            // every MMA issued has completed
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* never = drain + 1;             // nothing completes it (testing)
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(never + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -131,6 +132,7 @@ __global__ void __launch_bounds__(threads(NT), ctas_per_sm(NT))
       tc::mbar_init(&dempty[b], kEpi);
     }
     tc::mbar_init(drain, 1);
+    tc::mbar_init(never, 1);
     *abort_flag = 0;
     tc::fence_mbar_init();
     tc::tma_prefetch_desc(&map_x);
@@ -199,7 +201,7 @@ __global__ void __launch_bounds__(threads(NT), ctas_per_sm(NT))
     const uint64_t sdesc0 = tc::smem_desc_rows16(tc::smem_u32(chunks));
     uint32_t ch = 0, it = 0, s = 0, phase = 0, g = 0;
     uint32_t old = 0, old_phase = 0;  // ring slot of stage g - 2
-    bool ok = true;
+    bool ok = injected_timeout(a, never, abort_flag);
     for (uint32_t i = first; ok && i < n_work; i += stride, ++it) {
       const Work w = next_work(i, ge);
       const uint32_t idesc = tc::idesc_mxf4(BX, (w.ny + STEP - 1) & ~(STEP - 1));
@@ -502,6 +504,13 @@ extern "C" {
 moe_status mxfp4_matmul(const uint8_t* a_q, const uint8_t* a_s, const uint8_t* b_q,
                         const uint8_t* b_s, int64_t M, int64_t N, int64_t K, float alpha,
                         void* out, int32_t out_type, int32_t* d_status, moe_stream stream) {
+  return mxfp4_matmul_ex(a_q, a_s, b_q, b_s, M, N, K, alpha, out, out_type, d_status, -1, stream);
+}
+
+moe_status mxfp4_matmul_ex(const uint8_t* a_q, const uint8_t* a_s, const uint8_t* b_q,
+                           const uint8_t* b_s, int64_t M, int64_t N, int64_t K, float alpha,
+                           void* out, int32_t out_type, int32_t* d_status,
+                           int32_t test_timeout_cta, moe_stream stream) {
   using namespace moe;
   if (M < 0 || N < 0 || M > kMaxRows || N > kMaxRows || K < 32 || K > kMaxK || K % 32)
     return MOE_ERR_SHAPE;
@@ -520,6 +529,7 @@ moe_status mxfp4_matmul(const uint8_t* a_q, const uint8_t* a_s, const uint8_t* b
   a.alpha = alpha;
   a.out = out;
   a.status = d_status;
+  a.fail_cta = test_timeout_cta;
   return run(a, out_type, b_q, a_q, M, static_cast<cudaStream_t>(stream));
 }
 

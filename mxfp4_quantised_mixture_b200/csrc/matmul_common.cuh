@@ -22,6 +22,7 @@ constexpr int kChunkSlots = 2;
 constexpr int kMaxStages = 8;
 constexpr int kTableBytes = 4 * (kMaxGroups + 2) * 4;  // group table
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
+constexpr uint64_t kTestWaitNs = 200000ull;  // the injected wait of test_timeout_cta
 constexpr int64_t kMaxTiles = (int64_t(1) << 31) - (1 << 16);  // tile numbers, and a grid past them
 
 enum Mode : int { kDense = 0, kGrouped = 1, kWgrad = 2 };
@@ -47,6 +48,7 @@ struct Args {
   float alpha;
   void* out;
   int32_t* status;
+  int fail_cta = -1;  // testing: this CTA's first wait gives up
 };
 
 // One output tile: B rows [x0, ..) (of matrix e where B has groups), A rows
@@ -84,6 +86,15 @@ __device__ __forceinline__ bool all_wait(uint64_t* bar, uint32_t parity, volatil
                                          int32_t* status) {
   if (__all_sync(0xFFFFFFFFu, tc::mbar_wait<CLUSTER>(bar, parity, abort, kWaitLimitNs))) return true;
   abort_cta(abort, status);
+  return false;
+}
+
+// Testing only: in CTA a.fail_cta the warp waits, briefly, on a barrier that
+// nothing completes, and gives up as a timeout would.  False once it has.
+__device__ __forceinline__ bool injected_timeout(const Args& a, uint64_t* never, volatile int* abort) {
+  if (static_cast<int>(blockIdx.x) != a.fail_cta) return true;
+  if (__all_sync(0xFFFFFFFFu, tc::mbar_wait(never, 0, abort, kTestWaitNs))) return true;
+  abort_cta(abort, a.status);
   return false;
 }
 

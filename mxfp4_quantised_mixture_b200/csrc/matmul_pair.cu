@@ -112,7 +112,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint64_t* dfull = sempty + kSlots;  // [2] accumulator complete
   uint64_t* dempty = dfull + 2;            // [2] accumulator read by both CTAs (first CTA)
   uint64_t* drain = dempty + 2;            // every MMA issued has completed
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* never = drain + 1;             // nothing completes it (testing)
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(never + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -132,6 +133,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tc::mbar_init(&dempty[b], 2 * kEpi);
     }
     tc::mbar_init(drain, 1);
+    tc::mbar_init(never, 1);
     *abort_flag = 0;
     tc::fence_mbar_init();
     tc::tma_prefetch_desc(&map_x);
@@ -189,10 +191,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tc::mbar_drain(&full[i % NS], (i / NS) & 1, kWaitLimitNs / 8);
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
+    bool ok = injected_timeout(a, never, abort_flag);
     if (rank == 0) {
       const uint64_t desc0 = tc::smem_desc_sw128(tc::smem_u32(smem));
       uint32_t it = 0, s = 0, phase = 0, slot = 0;
-      bool ok = true, any = false;
+      bool any = false;
       for (uint32_t i = first; ok && i < n_work; i += stride, ++it) {
         const Work w = work_of<NT, STEP, BX>(a, grp, i, ge);
         const uint32_t idesc = tc::idesc_mxf4(BX, (w.ny + STEP - 1) & ~(STEP - 1));
@@ -251,7 +254,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // read them (the tcgen05 fences order tensor memory only)
       const uint32_t to = tc::cluster_addr(ready, 0);
       uint32_t s = 0, phase = 0;
-      bool ok = true;
       for (uint32_t i = first; ok && i < n_work; i += stride) {
         const int nst = pair_stages(work_of<NT, STEP, BX>(a, grp, i, ge));
         for (int st = 0; ok && st < nst; ++st) {
