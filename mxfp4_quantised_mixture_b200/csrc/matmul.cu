@@ -17,8 +17,8 @@
 // warp's stores are contiguous with no staging, and a decode batch of a few
 // rows costs the tensor core only those rows.
 //
-// With few tiles a cluster of CTAs shares each one's k range; the partial sums
-// meet in shared memory and are added in rank order.
+// With few tiles a cluster of CTAs shares each one's k range, if it is long; the
+// partial sums meet in shared memory and are added in rank order.
 //
 // What bounds it: with few rows to an expert the weights' way from HBM.  The 20B
 // decode batch's gate/up products (256 rows, 32 experts, 5760 x 2880: 285 MB)
@@ -76,6 +76,17 @@ __host__ __device__ constexpr int stages(int NT) {
 }
 __host__ __device__ constexpr int smem_bytes(int NT) {
   return 1024 + stages(NT) * stage_bytes(NT) + kChunkSlots * kChunkBytes + kTableBytes + 512;
+}
+
+// Whether a tile of nst stages is worth sharing between `split` CTAs.  Their two
+// meetings and the sum cost 1 us with 32 rows of A to a tile, 2 with 64 and 2.5
+// with 128, a stage takes 0.42 us, so sharing has to take 6 (9) stages off a CTA:
+// 64 x 1024 takes at K = 1024 (4 stages) 7.4 us alone and 8.2 shared, at 2048 9.0
+// and 8.6, at 8192 19.5 and 9.6; 128 x 1024 7.8 and 9.4, 9.8 and 10.3, 20.5 and
+// 11.7; eight groups of 1024 positions, 256 x 256 each, 9.4 and 11.4.
+template <int NT>
+__host__ __device__ constexpr bool sharing_pays(int nst, int split) {
+  return nst - (nst + split - 1) / split >= (NT > 64 ? 9 : 6);
 }
 
 // Columns [c0, c1) of the accumulator as fp32 into shared memory, [column][lane].
@@ -147,14 +158,22 @@ __global__ void __launch_bounds__(threads(NT), ctas_per_sm(NT))
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  const uint32_t n_work = tiles(a, grp);
-  // with a split, the CTAs of a cluster take one tile, each its share of k
+  uint32_t n_work = tiles(a, grp);
+  // with a split, the CTAs of a cluster take one tile, each its share of k, or the
+  // first of them the whole of a short one
   const uint32_t split = static_cast<uint32_t>(a.split);
   const uint32_t rank = split > 1 ? tc::cluster_rank() : 0u;
   const uint32_t first = blockIdx.x / split, stride = gridDim.x / split;
+  bool shared = false;
+  if (split > 1 && first < n_work) {
+    int e = 0;  // the host knows every length but those of a weight gradient's groups
+    shared = a.mode != kWgrad ||
+             sharing_pays<NT>(stages_of(work_of<NT, STEP, BX>(a, grp, first, e)), a.split);
+    if (!shared && rank > 0) n_work = 0;
+  }
   const auto next_work = [&](uint32_t i, int& e) {
     Work w = work_of<NT, STEP, BX>(a, grp, i, e);
-    if (split > 1) {
+    if (shared) {
       const int nst = stages_of(w);
       const int s0 = static_cast<int>(rank) * nst / a.split, s1 = static_cast<int>(rank + 1) * nst / a.split;
       w.k0 += s0 * kStepsPerStage * 64;
@@ -316,7 +335,7 @@ __global__ void __launch_bounds__(threads(NT), ctas_per_sm(NT))
       const int all = (w.ny + 15) & ~15;
       const int half = kEpi == 8 ? (all / 2 + 31) & ~31 : all;
       const int c0 = part ? min(half, all) : 0, c1 = part ? all : min(half, all);
-      if (split == 1)
+      if (!shared)
         store_columns<OUT>(acc, a, w, n, c0, c1);
       else
         stage_columns(acc, w, reinterpret_cast<float*>(smem), q * 32 + lane, c0, c1);
@@ -328,11 +347,11 @@ __global__ void __launch_bounds__(threads(NT), ctas_per_sm(NT))
 
   tc::tc_fence_before();
   __syncthreads();
-  if (split > 1) {
+  if (shared) {
     // every CTA's share of the sum lies in its ring's memory (its MMAs are done
     // with it); the columns are shared out and each is added up in rank order
     tc::cluster_sync();
-    if (first < n_work && *abort_flag == 0) {
+    if (*abort_flag == 0) {
       int e = 0;
       const Work w = work_of<NT, STEP, BX>(a, grp, first, e);
       // 32 threads to a column of 128, four neighbours each
@@ -434,13 +453,16 @@ moe_status launch_one(Args a, const uint8_t* xq, const uint8_t* yq, cudaStream_t
     return MOE_ERR_CUDA;
   // Few tiles leave most SMs without one: a cluster of up to 8 CTAs shares each
   // tile's k range, as long as a CTA keeps two stages of it and all the clusters
-  // run at once (23 clusters of 6 do not: 22 fit, and the last would wait).
+  // run at once (23 clusters of 6 do not: 22 fit, and the last would wait).  Of a
+  // weight gradient only the positions of all groups are known here: a cluster
+  // whose group is short leaves it to one CTA.
   const int64_t sms = sm_count(), nst = (a.K + kStepsPerStage * 64 - 1) / (kStepsPerStage * 64);
   int64_t split = sms / max_work;
   if (split > nst / 2) split = nst / 2;
   if (split > 8) split = 8;
   while (split > 1 && clusters_at_once<NT, OUT>(dev, static_cast<int>(split)) < max_work) --split;
-  a.split = split < 2 ? 1 : static_cast<int>(split);
+  a.split = split > 1 && sharing_pays<NT>(static_cast<int>(nst), static_cast<int>(split))
+                ? static_cast<int>(split) : 1;
   const int64_t cap = sms * ctas_per_sm(NT);
   const int64_t ctas = a.split > 1 ? max_work * a.split : (max_work < cap ? max_work : cap);
   ClusterLaunch l(static_cast<unsigned>(ctas), threads(NT), smem_bytes(NT), a.split, stream);
@@ -466,10 +488,11 @@ moe_status launch_nt(const Args& a, int out_type, const uint8_t* xq, const uint8
 // reads its weights again).  32 experts of 5760 x 2880 with 8, 30, 60 rows each:
 // tiles of 32 rows take 52, 54, 83 us, of 64 rows 53, 55, 58 us, of 128 rows (one
 // CTA per SM) 68, 69, 70 us, 16-row tiles 54 us and more throughout.
-// More than 128 rows take the CTA pairs, unless so few 128 x 128 tiles come of it
-// that three CTAs and more can share each one's k: 300 x 300 x 16384 then takes 13
-// us instead of 26, 1000 x 600 x 8192 15 instead of 18, while 512 x 2880 x 8192,
-// at 92 tiles, takes 21 instead of 18.5.
+// More than 128 rows take the CTA pairs, unless they are so few 128 x 128 tiles
+// that two thirds of the SMs would have none: 300 x 300 takes 8.2 instead of 8.9
+// us at K = 1024 and 13 instead of 26 at 16384, 800 x 700 8.6 instead of 9.2 at
+// 1024 and 12.8 instead of 12.7 at 4096, 1000 x 600 x 8192 15 instead of 18; 512 x
+// 2880 x 8192, at 92 tiles, takes 21 instead of 18.5.
 moe_status run(const Args& a, int out_type, const uint8_t* xq, const uint8_t* yq, int64_t rows,
                cudaStream_t stream) {
   if (rows > 128 && a.x_rows > 128) {
