@@ -484,10 +484,19 @@ moe_status launch_nt(const Args& a, int out_type, const uint8_t* xq, const uint8
 }
 
 // Rows of A per tile: `rows` is what one tile may meet, twice the mean of a
-// group where there are groups (so that few groups need a second tile, which
-// reads its weights again).  32 experts of 5760 x 2880 with 8, 30, 60 rows each:
-// tiles of 32 rows take 52, 54, 83 us, of 64 rows 53, 55, 58 us, of 128 rows (one
-// CTA per SM) 68, 69, 70 us, 16-row tiles 54 us and more throughout.
+// group where there are groups (few of which then need a second tile, which reads
+// its weights again).  Groups of up to 128 take 64 even so: two CTAs of an SM hide
+// each other's waits, which one of 128 rows does not.  us by tile width, bf16 out:
+//   32 experts of 5760 x 2880           32 rows   64   128   pairs
+//     8 rows each                          54     54    72    57
+//     8 on average, one expert has 132     57     59    78    58
+//     20 each                              55     57    80    63
+//     20, falling from 173                 66     62    83    61
+//     40 each                              86     59    78    64
+//     40, falling from 329                 81     70    86    69
+//     60 each                              87     61    80    67
+//   128 such experts, 60 each             344    212   306   240
+// (16-row tiles: 54 us and more throughout.)
 // More than 128 rows take the CTA pairs, unless they are so few 128 x 128 tiles
 // that two thirds of the SMs would have none: 300 x 300 takes 8.2 instead of 8.9
 // us at K = 1024 and 13 instead of 26 at 16384, 800 x 700 8.6 instead of 9.2 at
@@ -499,7 +508,7 @@ moe_status run(const Args& a, int out_type, const uint8_t* xq, const uint8_t* yq
     Args few = a;
     if (3 * plan_tiles(&few, BX, 128) > sm_count()) return launch_pair(a, out_type, xq, yq, stream);
   }
-  const int NT = rows <= 32 ? 32 : (rows <= 64 ? 64 : 128);
+  const int NT = rows <= 32 ? 32 : (rows <= (a.mode == kGrouped ? 128 : 64) ? 64 : 128);
   switch (NT) {
     case 32: return launch_nt<32>(a, out_type, xq, yq, stream);
     case 64: return launch_nt<64>(a, out_type, xq, yq, stream);
