@@ -360,7 +360,7 @@ MOE_API moe_status mxfp4_quantize_transposed(const uint16_t* w_bf16, int64_t bat
  * start at 128 * sum over i < e of ceil(count_i / 128); no block and no group
  * of 128 positions meets two groups.  A group's positions from its last row to
  * the next multiple of 128 are zero; positions behind the last group are left
- * as they were (mxfp4_matmul_grouped_wgrad reads none of them).
+ * as they were (no result of mxfp4_matmul_grouped_wgrad depends on them).
  *   w_bf16   in   [rows][cols] bf16, rows and cols as above with batch = 1
  *   offsets  in   [E+1] device, ascending, in [0, rows], 1 <= E <= 256; rows in
  *                 no group are not read

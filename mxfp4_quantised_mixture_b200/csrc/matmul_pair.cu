@@ -22,10 +22,9 @@
 // the copy ring's own queue.)  Waits and issue stay with whole warps and an
 // elected lane: under `lane == 0` four MMAs and one wait took 480 cycles instead
 // of 245.  Arrivals on the other CTA's barriers release this CTA's shared memory
-// at cluster scope by a fence for it alone: as mbarrier.arrive.release.cluster
-// they cost a fifth of the time (dense 8192 x 5760 x 2880 in a loop: the second
-// CTA's copies alone by that form 93 us, the scale writers' arrivals too 114,
-// against 81 by the fence).
+// at cluster scope by a fence for it alone, which costs nothing measurable.  With
+// mbarrier.arrive.release.cluster the same product took 93 us in a loop for the
+// second CTA's copies alone and 114 for the scale writers' arrivals too, against 81.
 //
 // Warp roles, in each CTA of the pair:
 //   warp 0       producer: per stage of 512 k its own 128 rows of B and its half
